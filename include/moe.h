@@ -101,8 +101,21 @@ typedef enum {
     MOE_STAGE_FORWARD = 4,
     MOE_STAGE_GATE_BACKWARD = 5,
     MOE_STAGE_FFN_BACKWARD = 6,
-    MOE_STAGE_FORWARD_FP8W = 7
+    MOE_STAGE_FORWARD_FP8W = 7,
+    MOE_STAGE_LINEAR = 8,          /* moe_linear_workspace_bytes */
+    MOE_STAGE_LINEAR_BACKWARD = 9  /* moe_linear_workspace_bytes */
 } moe_stage;
+
+/* the activation of a linear layer: gelu(z) = z Phi(z) (the exact form, Phi
+ * the normal distribution's integral), silu(z) = z / (1 + exp(-z)) */
+typedef enum { MOE_FN_NONE = 0, MOE_FN_RELU = 1, MOE_FN_GELU = 2, MOE_FN_SILU = 3 } moe_fn;
+
+/* how a linear layer's forward keeps its pre-activations for the backward */
+typedef enum {
+    MOE_SAVE_NONE = 0,
+    MOE_SAVE_ACT = 1, /* in the act type */
+    MOE_SAVE_INT8 = 2 /* in 8 bits (the rows8 format, see moe_pack_rows8) */
+} moe_save;
 
 typedef struct {
     int64_t T;        /* tokens on this GPU */
@@ -123,6 +136,21 @@ typedef struct {
     int32_t quant;    /* moe_quant, with dispatch = MOE_FP8_E4M3 only (else it
                          must be MOE_QUANT_TOKEN) */
 } moe_shape;
+
+/* A linear layer over rows sorted by group (moe_grouped_linear), or with one
+ * weight matrix (moe_linear: groups = 1). Limits: 0 <= rows < 2^31, n_in and
+ * n_out at most 2^20 and multiples of 8 (act = MOE_BF16) or 4 (MOE_F32), so
+ * that every row moves as 16-byte pieces; 1 <= groups <= 256. */
+typedef struct {
+    int64_t rows;   /* rows of x and y */
+    int32_t n_in;   /* values of an input row */
+    int32_t n_out;  /* values of an output row */
+    int32_t groups; /* weight matrices */
+    int32_t act;    /* moe_dtype of x, w, residual, y, dy and dx */
+    int32_t fn;     /* moe_fn */
+    int32_t save;   /* moe_save */
+    int32_t grad;   /* moe_dtype of dw and db: MOE_F32 or act */
+} moe_linear_shape;
 
 /* Host only. Bytes of workspace that `stage` needs for shape *s (0 when the
  * stage needs none), or 0 for an invalid shape. */
@@ -460,6 +488,91 @@ int32_t moe_forward_traced(const moe_shape *s, const void *x, const void *w_gate
  * gate's name is "gate_two_phase" when *s takes the two-phase gate. */
 int32_t moe_forward_kernel_count(const moe_shape *s);
 const char *moe_forward_kernel_name(const moe_shape *s, int32_t i);
+
+/*
+ * Linear layers: the products that surround or replace the SwiGLU experts
+ * (another expert form, a projection per expert, the dense projections and
+ * feed-forward layers next to the MoE layer), with their bias, activation and
+ * residual in the product's epilogue.
+ *
+ * moe_grouped_linear: group g holds rows offsets[g] .. offsets[g+1]-1 (int32
+ *  [groups+1], as moe_dispatch writes them), and for each of its rows
+ *    z[r] = w_g x[r] + bias_g,   y[r] = fn(z[r]) + residual[r]
+ *  x [rows, n_in], w [groups, n_out, n_in], y and residual [rows, n_out]
+ *  (act); bias [groups, n_out] float32 or NULL; residual may be NULL, or y
+ *  itself. Sums, bias, activation and residual in float32, y rounded once.
+ *  Rows of no group (before offsets[0], from offsets[groups] on) are left as
+ *  they were. Offsets outside [0, rows] or decreasing are detected on the
+ *  device: they are taken into the range and to the largest so far, no memory
+ *  outside the buffers is touched, and the workspace's sticky flag is set
+ *  (moe_get_device_error: MOE_ERR_BAD_INDEX).
+ *  saved (save != MOE_SAVE_NONE; 256-byte aligned, moe_linear_saved_bytes
+ *  bytes) receives z for the backward: [rows, n_out] in the act type, or in 8
+ *  bits as the rows8 format (quantised from the float32 sums).
+ * moe_linear: the same with one weight matrix w [n_out, n_in] and bias
+ *  [n_out]; groups must be 1.
+ * moe_grouped_linear_backward: with zs the pre-activations as saved (fn !=
+ *  MOE_FN_NONE: save must not be MOE_SAVE_NONE),
+ *    dz[r] = dy[r] fn'(zs[r]),  dx[r] = dz[r] w_g  (act, [rows, n_in]),
+ *    dw_g = sum_r dz[r]^T x[r]  ([groups, n_out, n_in]),
+ *    db_g = sum_r dz[r]         ([groups, n_out]), both in the `grad` type.
+ *  The gradient of the residual is dy itself. dx, dw and db may be NULL (not
+ *  computed); w is needed for dx, x for dw. relu'(0) = 0. dz is rounded to
+ *  the act type before the products (bf16: their operands), db sums it
+ *  before that; each output is rounded once. dw and db are overwritten, and
+ *  zero for a group without rows; every call gives the same bits (no float
+ *  atomics). x must be the forward's input and `saved` what it wrote.
+ * moe_linear_backward: the same with one weight matrix.
+ * ws: moe_linear_workspace_bytes for MOE_STAGE_LINEAR or
+ *  MOE_STAGE_LINEAR_BACKWARD (host only; at least the 256-byte header; 0 for
+ *  an invalid shape), cleared once by moe_workspace_init. A workspace serves
+ *  one call at a time: calls that may overlap need one each.
+ * moe_linear_saved_bytes: host only; 0 with MOE_SAVE_NONE or an invalid shape.
+ * rows = 0 is valid: the forward enqueues nothing, the backward zeroes dw and
+ *  db. Errors: MOE_ERR_INVALID_ARG (bad sizes, a NULL or misaligned pointer,
+ *  a missing or short `saved`), MOE_ERR_UNSUPPORTED (outside the limits),
+ *  MOE_ERR_WORKSPACE, MOE_ERR_HIP.
+ */
+size_t moe_linear_workspace_bytes(const moe_linear_shape *s, int32_t stage);
+size_t moe_linear_saved_bytes(const moe_linear_shape *s);
+int32_t moe_grouped_linear(const moe_linear_shape *s, const void *x, const int32_t *offsets,
+                           const void *w, const float *bias, const void *residual, void *y,
+                           void *saved, size_t saved_bytes, void *ws, size_t ws_bytes,
+                           void *stream);
+int32_t moe_linear(const moe_linear_shape *s, const void *x, const void *w, const float *bias,
+                   const void *residual, void *y, void *saved, size_t saved_bytes, void *ws,
+                   size_t ws_bytes, void *stream);
+int32_t moe_grouped_linear_backward(const moe_linear_shape *s, const void *x,
+                                    const int32_t *offsets, const void *w, const void *saved,
+                                    size_t saved_bytes, const void *dy, void *dx, void *dw,
+                                    void *db, void *ws, size_t ws_bytes, void *stream);
+int32_t moe_linear_backward(const moe_linear_shape *s, const void *x, const void *w,
+                            const void *saved, size_t saved_bytes, const void *dy, void *dx,
+                            void *dw, void *db, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The rows8 format: activation checkpoints in 8 bits. Every 32 consecutive
+ * values of a row (the last block of a row may be shorter) share a step 2^e,
+ * e the smallest integer with max|v| <= 127 * 2^e, not below -126; a value is
+ * the int8 code round-to-nearest-even(v / 2^e) in [-127, 127]. Reading back
+ * gives code * 2^e, exact in bf16 and float32, at most 2^e / 2 <= max|v| / 127
+ * away from v. A block that holds an infinity or a NaN reads back as NaN.
+ * Layout of `rows` rows of n values: codes [rows, n32] (n32 = n rounded up to
+ * 32, padding codes 0), then at the next multiple of 256 bytes the scale
+ * bytes e + 127 (255: not finite) [rows, n32 / 32].
+ *
+ * moe_rows8_bytes: host only; the buffer's size, a multiple of 256 (0 for
+ *  rows < 0, n < 1 or n > 2^20).
+ * moe_pack_rows8 / moe_unpack_rows8: x [rows, n] of dtype (MOE_F32 or
+ *  MOE_BF16; any n), 16-byte aligned, to / from `packed`, 256-byte aligned.
+ *  rows = 0 enqueues nothing. Errors: MOE_ERR_INVALID_ARG (sizes, pointers,
+ *  a short buffer), MOE_ERR_UNSUPPORTED (dtype), MOE_ERR_HIP.
+ */
+size_t moe_rows8_bytes(int64_t rows, int32_t n);
+int32_t moe_pack_rows8(int64_t rows, int32_t n, int32_t dtype, const void *x, void *packed,
+                       size_t packed_bytes, void *stream);
+int32_t moe_unpack_rows8(int64_t rows, int32_t n, int32_t dtype, const void *packed,
+                         size_t packed_bytes, void *x, void *stream);
 
 /* Reads and clears the workspace's sticky device error flag. This call
  * synchronises `stream`. Returns MOE_OK or MOE_ERR_BAD_INDEX (or an error). */

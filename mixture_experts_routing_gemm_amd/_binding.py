@@ -30,6 +30,8 @@ STAGE_GATE, STAGE_DISPATCH, STAGE_FFN, STAGE_COMBINE, STAGE_FORWARD = 0, 1, 2, 3
 STAGE_GATE_BACKWARD = 5
 STAGE_FFN_BACKWARD = 6
 STAGE_FORWARD_FP8W = 7
+STAGE_LINEAR = 8
+STAGE_LINEAR_BACKWARD = 9
 FP8W_KERNELS = ["gate_topk", "dispatch_rank", "dispatch_scan", "dispatch_permute_fp8", "ffn_plan",
                 "ffn_up", "ffn_hidden_quant", "ffn_down", "combine"]
 
@@ -55,6 +57,20 @@ class moe_shape(ctypes.Structure):
                 f"overflow={self.overflow}, quant={self.quant})")
 
 
+class moe_linear_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("act", ctypes.c_int32), ("fn", ctypes.c_int32),
+                ("save", ctypes.c_int32), ("grad", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"moe_linear_shape(rows={self.rows}, n_in={self.n_in}, n_out={self.n_out}, "
+                f"groups={self.groups}, act={self.act}, fn={self.fn}, save={self.save}, grad={self.grad})")
+
+
+MOE_FN_NONE, MOE_FN_RELU, MOE_FN_GELU, MOE_FN_SILU = 0, 1, 2, 3
+MOE_SAVE_NONE, MOE_SAVE_ACT, MOE_SAVE_INT8 = 0, 1, 2
+_FN = {"none": MOE_FN_NONE, "relu": MOE_FN_RELU, "gelu": MOE_FN_GELU, "silu": MOE_FN_SILU}
+_SAVE = {"none": MOE_SAVE_NONE, "act": MOE_SAVE_ACT, "int8": MOE_SAVE_INT8}
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_REASSIGN = 0, 1
 MOE_QUANT_TOKEN, MOE_QUANT_EXPERT, MOE_QUANT_GLOBAL, MOE_QUANT_TOKEN_ABSMAX = 0, 1, 2, 3
 _QUANT = {"token": MOE_QUANT_TOKEN, "expert": MOE_QUANT_EXPERT, "global": MOE_QUANT_GLOBAL,
@@ -71,6 +87,16 @@ def make_shape(T, d, E, k, S, h, act="bf16", dispatch=None, capacity=0,
     q = _QUANT[quant] if isinstance(quant, str) else int(quant)
     return moe_shape(int(T), int(d), int(E), int(k), int(S), int(h), a, dsp, int(capacity),
                      MOE_OVERFLOW_REASSIGN if reassign else MOE_OVERFLOW_DROP, q)
+
+
+def make_linear_shape(rows, n_in, n_out, groups=1, act="bf16", fn="none", save="none",
+                      grad="f32") -> moe_linear_shape:
+    """A linear layer's shape. act, grad: "f32" or "bf16"; fn: "none", "relu", "gelu" or "silu";
+    save (the pre-activations kept for the backward): "none", "act" or "int8"."""
+    def code(v, names):
+        return names[v] if isinstance(v, str) else int(v)
+    return moe_linear_shape(int(rows), int(n_in), int(n_out), int(groups), code(act, _DTYPES),
+                            code(fn, _FN), code(save, _SAVE), code(grad, _DTYPES))
 
 
 def shape_of(cfg) -> moe_shape:
@@ -136,6 +162,25 @@ def _load():
     L.moe_forward_kernel_count.restype = i32
     L.moe_forward_kernel_name.argtypes = [sp, i32]
     L.moe_forward_kernel_name.restype = ctypes.c_char_p
+    lp, i64 = ctypes.POINTER(moe_linear_shape), ctypes.c_int64
+    L.moe_linear_workspace_bytes.argtypes = [lp, i32]
+    L.moe_linear_workspace_bytes.restype = sz
+    L.moe_linear_saved_bytes.argtypes = [lp]
+    L.moe_linear_saved_bytes.restype = sz
+    L.moe_grouped_linear.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp]
+    L.moe_grouped_linear.restype = i32
+    L.moe_linear.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp]
+    L.moe_linear.restype = i32
+    L.moe_grouped_linear_backward.argtypes = [lp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_grouped_linear_backward.restype = i32
+    L.moe_linear_backward.argtypes = [lp, vp, vp, vp, sz, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_linear_backward.restype = i32
+    L.moe_rows8_bytes.argtypes = [i64, i32]
+    L.moe_rows8_bytes.restype = sz
+    L.moe_pack_rows8.argtypes = [i64, i32, i32, vp, vp, sz, vp]
+    L.moe_pack_rows8.restype = i32
+    L.moe_unpack_rows8.argtypes = [i64, i32, i32, vp, sz, vp, vp]
+    L.moe_unpack_rows8.restype = i32
     L.moe_get_device_error.argtypes = [vp, sz, vp]
     L.moe_get_device_error.restype = i32
     return L
@@ -148,7 +193,10 @@ EXPORTS = ["moe_workspace_bytes", "moe_workspace_init", "moe_status_string", "mo
            "moe_dispatch_backward", "moe_gate_backward", "moe_grouped_ffn_backward", "moe_forward", "moe_forward_traced",
            "moe_forward_kernel_count", "moe_forward_kernel_name", "moe_get_device_error",
            "moe_fp8_weight_scale_floats", "moe_quantize_weights", "moe_forward_fp8w",
-           "moe_ffn_saved_bytes", "moe_grouped_ffn_save", "moe_grouped_ffn_backward_saved"]
+           "moe_ffn_saved_bytes", "moe_grouped_ffn_save", "moe_grouped_ffn_backward_saved",
+           "moe_linear_workspace_bytes", "moe_linear_saved_bytes", "moe_grouped_linear", "moe_linear",
+           "moe_grouped_linear_backward", "moe_linear_backward", "moe_rows8_bytes", "moe_pack_rows8",
+           "moe_unpack_rows8"]
 
 
 def status_string(status: int) -> str:
@@ -355,3 +403,130 @@ def moe_get_device_error(ws, stream=None) -> int:
     """Reads and clears the sticky device flag (synchronises the stream)."""
     wp, wn = _ws(ws)
     return int(lib.moe_get_device_error(wp, wn, _s(stream)))
+
+
+# ------------------------------------------------------------ linear layers --
+_TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _t(t, dtype, numel, name):
+    """The pointer of a tensor that must be there, of this type and size, on the current GPU."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or t.numel() != numel:
+        raise ValueError(f"{name}: expected {numel} values of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return _p(t)
+
+
+def _t0(t, dtype, numel, name):
+    return None if t is None else _t(t, dtype, numel, name)
+
+
+def moe_linear_workspace_bytes(shape: moe_linear_shape, stage: int) -> int:
+    return int(lib.moe_linear_workspace_bytes(ctypes.byref(shape), int(stage)))
+
+
+def moe_linear_saved_bytes(shape: moe_linear_shape) -> int:
+    return int(lib.moe_linear_saved_bytes(ctypes.byref(shape)))
+
+
+def alloc_linear_workspace(shape: moe_linear_shape, stage: int, device="cuda", stream=None):
+    """A zero-headed workspace for `stage` (STAGE_LINEAR or STAGE_LINEAR_BACKWARD)."""
+    n = moe_linear_workspace_bytes(shape, stage)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_linear_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def alloc_linear_saved(shape: moe_linear_shape, device="cuda"):
+    """The buffer of saved pre-activations (uint8; None when the shape saves none)."""
+    n = moe_linear_saved_bytes(shape)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _linear_operands(s):
+    act = _TORCH.get(s.act)
+    if act is None:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "linear layer: act")
+    return act, s.rows * s.n_in, s.rows * s.n_out, s.groups * s.n_in * s.n_out
+
+
+def moe_grouped_linear(shape, x, offsets, w, bias, residual, y, saved, ws, stream=None):
+    act, nx, ny, nw = _linear_operands(shape)
+    sv, sn = _ws(saved)
+    wp, wn = _ws(ws)
+    _check(lib.moe_grouped_linear(
+        ctypes.byref(shape), _t(x, act, nx, "x"), _t(offsets, torch.int32, shape.groups + 1, "offsets"),
+        _t(w, act, nw, "w"), _t0(bias, torch.float32, shape.groups * shape.n_out, "bias"),
+        _t0(residual, act, ny, "residual"), _t(y, act, ny, "y"), sv, sn, wp, wn, _s(stream)),
+        "moe_grouped_linear")
+
+
+def moe_linear(shape, x, w, bias, residual, y, saved, ws, stream=None):
+    act, nx, ny, nw = _linear_operands(shape)
+    sv, sn = _ws(saved)
+    wp, wn = _ws(ws)
+    _check(lib.moe_linear(
+        ctypes.byref(shape), _t(x, act, nx, "x"), _t(w, act, nw, "w"),
+        _t0(bias, torch.float32, shape.groups * shape.n_out, "bias"), _t0(residual, act, ny, "residual"),
+        _t(y, act, ny, "y"), sv, sn, wp, wn, _s(stream)), "moe_linear")
+
+
+def _linear_backward(name, shape, x, offsets, w, saved, dy, dx, dw, db, ws, stream):
+    act, nx, ny, nw = _linear_operands(shape)
+    grad = _TORCH.get(shape.grad)
+    sv, sn = _ws(saved)
+    wp, wn = _ws(ws)
+    off = () if offsets is None else (_t(offsets, torch.int32, shape.groups + 1, "offsets"),)
+    _check(getattr(lib, name)(
+        ctypes.byref(shape), _t0(x, act, nx, "x"), *off, _t0(w, act, nw, "w"), sv, sn,
+        _t0(dy, act, ny, "dy"), _t0(dx, act, nx, "dx"), _t0(dw, grad, nw, "dw"),
+        _t0(db, grad, shape.groups * shape.n_out, "db"), wp, wn, _s(stream)), name)
+
+
+def moe_grouped_linear_backward(shape, x, offsets, w, saved, dy, dx, dw, db, ws, stream=None):
+    if offsets is None:
+        raise ValueError("offsets is required")
+    _linear_backward("moe_grouped_linear_backward", shape, x, offsets, w, saved, dy, dx, dw, db, ws, stream)
+
+
+def moe_linear_backward(shape, x, w, saved, dy, dx, dw, db, ws, stream=None):
+    _linear_backward("moe_linear_backward", shape, x, None, w, saved, dy, dx, dw, db, ws, stream)
+
+
+# ---------------------------------------------------------- 8-bit checkpoints --
+def moe_rows8_bytes(rows: int, n: int) -> int:
+    return int(lib.moe_rows8_bytes(int(rows), int(n)))
+
+
+def alloc_rows8(rows, n, device="cuda"):
+    """The buffer of `rows` packed rows of n values (uint8)."""
+    size = moe_rows8_bytes(rows, n)
+    if size == 0 and rows != 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_rows8_bytes")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _rows8(x):
+    if x.dim() != 2:
+        raise ValueError(f"expected rows [rows, n], got {tuple(x.shape)}")
+    for code, dtype in _TORCH.items():
+        if x.dtype == dtype:
+            return int(x.shape[0]), int(x.shape[1]), code
+    raise MoEError(MOE_ERR_UNSUPPORTED, f"rows of {x.dtype}")
+
+
+def moe_pack_rows8(x, packed, stream=None):
+    rows, n, code = _rows8(x)
+    pp, pn = _ws(packed)
+    _check(lib.moe_pack_rows8(rows, n, code, _p(x), pp, pn, _s(stream)), "moe_pack_rows8")
+
+
+def moe_unpack_rows8(packed, x, stream=None):
+    rows, n, code = _rows8(x)
+    pp, pn = _ws(packed)
+    _check(lib.moe_unpack_rows8(rows, n, code, pp, pn, _p(x), _s(stream)), "moe_unpack_rows8")

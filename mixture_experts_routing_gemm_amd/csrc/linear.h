@@ -1,0 +1,457 @@
+// What the linear layer's kernels share: the arguments, the walk over ragged
+// groups, the activation functions and the epilogue.
+//
+// The layer: rows x [R, K] sorted by group, group g holding the rows
+// offsets[g] .. offsets[g+1]-1 (one group of all R rows without offsets), and
+//     z[r] = W_g x[r] + b_g,   y[r] = fn(z[r]) + residual[r]
+// with W [G, N, K]; backward, with zs the pre-activation as it was saved,
+//     dz = dy fn'(zs),  dx[r] = dz[r] W_g,  dW_g = sum_r dz[r] x[r]^T,
+//     db_g = sum_r dz[r].
+// One tile kernel computes C [M, N] = sum_k A(m, k) B(n, k) for all three:
+//     forward  A = x rows,   B = W_g rows        (both contiguous along k)
+//     dx       A = dz rows,  B = W_g columns     (B contiguous along n)
+//     dW       A = dz cols,  B = x columns       (both contiguous along m / n,
+//                                                 k runs over the group's rows)
+#pragma once
+
+#include "moe_device.h"
+#include "rows8.h"
+
+namespace moe {
+
+constexpr int kMaxGroups = 256;
+
+enum LinearPass { kLinForward = 0, kLinDx = 1, kLinDw = 2 };
+
+struct LinearArgs {
+    const uint8_t* a;        // x (forward), dz (dx, dW)
+    const uint8_t* b;        // W (forward, dx), x (dW)
+    const int32_t* offsets;  // [G+1], NULL: one group of R rows
+    uint32_t* hdr;           // error flag of the workspace, or NULL
+    int64_t R;
+    int G;
+    int M, N, K;             // M: dW only (n_out); K: forward and dx
+    int mtiles, ntn;         // dW: m-tiles a group; n-tiles
+    // epilogue
+    int fn;
+    const float* bias;       // [G, N] or NULL
+    const uint8_t* residual; // [R, N] (act) or NULL
+    uint8_t* out;            // y / dx [R, N] (act), dW [G, M, N] (act or float32)
+    uint8_t* zsave;          // saved pre-activations [R, N] (act), or NULL
+    uint8_t* codes;          // saved pre-activations in 8 bits, or NULL
+    uint8_t* scales;
+    int64_t n32;             // row stride of the codes
+    int out_f32;             // dW: float32 output
+    // split along k: part s of `parts` writes its float32 sums to
+    // part_out [parts][rows][N] (rows: R, or G * M for dW), joined later
+    float* part_out;
+    int parts;
+};
+
+// ------------------------------------------------------------ functions --
+__device__ __forceinline__ float lin_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+
+// Phi(v), the normal distribution's integral, from Abramowitz and Stegun's
+// formula 7.1.26 for erf (off by at most 1.5e-7): with x = |v| / sqrt(2) and
+// t = 1 / (1 + 0.3275911 x), erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5))))
+// e^(-x x). Also gives e = e^(-v v / 2), which the slope needs too.
+__device__ __forceinline__ float normal_cdf(float v, float& e) {
+    const float x = __builtin_fabsf(v) * 0.70710678118654752f;
+    e = __expf(-x * x);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+    float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+    p = __builtin_fmaf(p, t, 1.421413741f);
+    p = __builtin_fmaf(p, t, -0.284496736f);
+    p = __builtin_fmaf(p, t, 0.254829592f);
+    const float half_tail = 0.5f * p * t * e;  // Phi(-|v|)
+    return v < 0.0f ? half_tail : 1.0f - half_tail;
+}
+
+// (the comparisons are written so that a NaN stays one, and gelu(-inf),
+// silu(-inf) are 0: the product of -inf with a zero would be a NaN)
+__device__ __forceinline__ float lin_fn(int fn, float z) {
+    if (fn == MOE_FN_RELU) return z < 0.0f ? 0.0f : z;
+    if (fn == MOE_FN_GELU) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return c == 0.0f ? 0.0f : z * c;
+    }
+    if (fn == MOE_FN_SILU) {
+        const float s = lin_sigmoid(z);
+        return s == 0.0f ? 0.0f : z * s;
+    }
+    return z;
+}
+__device__ __forceinline__ float lin_slope(int fn, float z) {
+    if (fn == MOE_FN_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if (fn == MOE_FN_GELU) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return e == 0.0f ? c : __builtin_fmaf(z * e, 0.39894228040143268f, c);
+    }
+    if (fn == MOE_FN_SILU) {
+        const float s = lin_sigmoid(z);
+        return s == 0.0f ? 0.0f : (s == 1.0f ? 1.0f : s * __builtin_fmaf(z, 1.0f - s, 1.0f));
+    }
+    return 1.0f;
+}
+
+// ------------------------------------------------------------ group walk --
+// Row ranges of the groups and the prefix of their m-tiles, in LDS. Offsets
+// are taken into [0, R] and made non-decreasing (each becomes the largest so
+// far), so that no row outside the buffers is ever touched; offsets that this
+// changes are reported through the workspace's error flag.
+struct GroupWalk {
+    int off[kMaxGroups + 1];
+    int pre[kMaxGroups + 1];
+};
+
+// by every thread of a work-group of at least one wave; ends with a barrier
+__device__ __forceinline__ void walk_groups(GroupWalk& w, const int32_t* __restrict__ offsets, int64_t R, int G,
+                                            int bm, uint32_t* hdr) {
+    const int R32 = static_cast<int>(R);
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        if (offsets == nullptr) {
+            if (lane == 0) {
+                w.off[0] = 0;
+                w.off[1] = R32;
+                w.pre[0] = 0;
+                w.pre[1] = (R32 + bm - 1) / bm;
+            }
+        } else {
+            // lane i holds entries per*i .. per*i + per-1 of the G + 1 offsets
+            const int per = (G + 1 + 63) / 64;  // at most 5
+            int v[5], run = 0;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int g = lane * per + i;
+                v[i] = 0;
+                if (i < per && g <= G) {
+                    const int raw = offsets[g];
+                    v[i] = min(max(raw, 0), R32);
+                    bad |= raw != v[i] || v[i] < run;
+                    run = max(run, v[i]);
+                    v[i] = run;
+                }
+            }
+            int top = run;  // running maximum over the lanes
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int t = __shfl_up(top, o, 64);
+                if (lane >= o) top = max(top, t);
+            }
+            int before = __shfl_up(top, 1, 64);
+            if (lane == 0) before = 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int g = lane * per + i;
+                if (i < per && g <= G) {
+                    bad |= v[i] < before;
+                    v[i] = max(v[i], before);
+                    w.off[g] = v[i];
+                }
+            }
+            if (bad && blockIdx.x == 0 && blockIdx.y == 0) set_error(hdr, 1u);
+            // (one wave: its LDS accesses complete in order)
+            __builtin_amdgcn_wave_barrier();
+            int sum = 0, t[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int g = lane * per + i;
+                t[i] = 0;
+                if (i < per && g < G) t[i] = (w.off[g + 1] - w.off[g] + bm - 1) / bm;
+                sum += t[i];
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int u = __shfl_up(incl, o, 64);
+                if (lane >= o) incl += u;
+            }
+            int acc = incl - sum;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int g = lane * per + i;
+                if (i < per && g <= G) w.pre[g] = acc;
+                acc += t[i];
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// the last g with pre[g] <= v (pre[0] = 0 <= v): every lane looks at every
+// 64th group
+__device__ __forceinline__ int group_of(const GroupWalk& w, int G, int v) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int i = 0; i < G; i += 64) {
+        const bool le = i + lane < G && w.pre[min(i + lane, G)] <= v;
+        n += __popcll(__ballot(le));
+    }
+    return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+// ------------------------------------------------------------- epilogue --
+// Eight float32 values of one row, stored as the output type; nv (0 .. 8) of
+// them exist (bf16: 0 or 8; float32: 0, 4 or 8).
+template <typename T>
+__device__ __forceinline__ void load8(const uint8_t* p, int64_t at, int nv, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<bf16_t>(const uint8_t* p, int64_t at, int, float (&v)[8]) {
+    ActVec<bf16_t>::unpack(load16(p + at * 2), v);
+}
+template <>
+__device__ __forceinline__ void load8<float>(const uint8_t* p, int64_t at, int nv, float (&v)[8]) {
+    ActVec<float>::unpack(load16(p + at * 4), v);
+    if (nv > 4) {
+        ActVec<float>::unpack(load16(p + at * 4 + 16), v + 4);
+    } else {
+#pragma unroll
+        for (int u = 4; u < 8; ++u) v[u] = 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(uint8_t* p, int64_t at, int nv, const float (&v)[8]);
+template <>
+__device__ __forceinline__ void store8<bf16_t>(uint8_t* p, int64_t at, int, const float (&v)[8]) {
+    store16(p + at * 2, ActVec<bf16_t>::pack(v));
+}
+template <>
+__device__ __forceinline__ void store8<float>(uint8_t* p, int64_t at, int nv, const float (&v)[8]) {
+    store16(p + at * 4, ActVec<float>::pack(v));
+    if (nv > 4) store16(p + at * 4 + 16, ActVec<float>::pack(v + 4));
+}
+
+// The 32 columns c0 .. c0+31 of one row of the forward's output, held by two
+// lanes (half = 0, 1): half h has columns c0 + 8 h .. +7 in v[0] and c0 + 16 +
+// 8 h .. +7 in v[1]. Adds the bias, keeps the pre-activation, applies fn, adds
+// the residual and stores. `ok`: the row exists (the same for both lanes; both
+// call this, whether it exists or not).
+template <typename T>
+__device__ __forceinline__ void linear_epilogue32(const LinearArgs& a, int g, int64_t row, int c0, int half,
+                                                  bool ok, float (&v)[2][8]) {
+    int nv[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        nv[p] = min(8, max(0, a.N - (c0 + 16 * p + 8 * half)));
+        if (!ok) nv[p] = 0;
+        if (a.bias != nullptr && nv[p] > 0) {
+            float b[8];
+            load8<float>(reinterpret_cast<const uint8_t*>(a.bias), static_cast<int64_t>(g) * a.N + c0 + 16 * p + 8 * half,
+                         nv[p], b);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[p][u] += b[u];
+        }
+    }
+    if (a.zsave != nullptr) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            if (nv[p] > 0) store8<T>(a.zsave, row * a.N + c0 + 16 * p + 8 * half, nv[p], v[p]);
+    }
+    if (a.codes != nullptr) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = max(top, u < nv[p] ? abs_bits(v[p][u]) : 0u);
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
+        if (ok && c0 < a.n32) {
+            const uint32_t scale = rows8_scale(top);
+            const float inv = rows8_inverse(scale);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float q[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) q[u] = u < nv[p] ? v[p][u] : 0.0f;  // the padding's codes are 0
+                uint2 w;
+                w.x = rows8_code4(q[0], q[1], q[2], q[3], inv);
+                w.y = rows8_code4(q[4], q[5], q[6], q[7], inv);
+                *reinterpret_cast<uint2*>(a.codes + row * a.n32 + c0 + 16 * p + 8 * half) = w;
+            }
+            if (half == 0) a.scales[row * (a.n32 / kRows8Block) + c0 / kRows8Block] = static_cast<uint8_t>(scale);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        if (nv[p] == 0) continue;
+        const int64_t at = row * a.N + c0 + 16 * p + 8 * half;
+        if (a.fn != MOE_FN_NONE) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[p][u] = lin_fn(a.fn, v[p][u]);
+        }
+        if (a.residual != nullptr) {
+            float r[8];
+            load8<T>(a.residual, at, nv[p], r);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[p][u] += r[u];
+        }
+        store8<T>(a.out, at, nv[p], v[p]);
+    }
+}
+
+// The same 32 columns of a row of dx (T), dW (T or float32) or of a part's
+// sums: stored as they are. `base`: elements before the row.
+template <typename T>
+__device__ __forceinline__ void plain_epilogue32(uint8_t* out, int64_t base, int N, int c0, int half, bool ok,
+                                                 const float (&v)[2][8]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int c = c0 + 16 * p + 8 * half;
+        const int nv = ok ? min(8, max(0, N - c)) : 0;
+        if (nv > 0) store8<T>(out, base + c, nv, v[p]);
+    }
+}
+
+// A 32x32 accumulator block, element 4 q + u of lane (lr, lg) being row lr and
+// column 8 q + 4 lg + u, as the two runs of eight columns that the epilogues
+// take: a half-wave swap per pair of column groups.
+__device__ __forceinline__ void block_runs(const f32x16& acc, float (&v)[2][8]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[8 * p + u]),
+                                                            __float_as_uint(acc[8 * p + 4 + u]), false, false);
+            v[p][u] = __uint_as_float(s[0]);
+            v[p][4 + u] = __uint_as_float(s[1]);
+        }
+}
+
+// The store of one 32x32 block of C at rows m0 + lr, columns c0 ..: `row0` is
+// the first row of the group (forward, dx), `rows` the rows that exist.
+template <typename T, int PASS>
+__device__ __forceinline__ void store_block(const LinearArgs& a, int g, int part, int64_t row0, int rows, int m,
+                                            int c0, int half, const f32x16& acc) {
+    float v[2][8];
+    block_runs(acc, v);
+    const bool ok = m < rows;
+    const int64_t row = row0 + m;
+    if (a.part_out != nullptr) {
+        const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
+        plain_epilogue32<float>(reinterpret_cast<uint8_t*>(a.part_out), (part * all + row) * a.N, a.N, c0, half, ok, v);
+    } else if constexpr (PASS == kLinForward) {
+        linear_epilogue32<T>(a, g, row, c0, half, ok, v);
+    } else if constexpr (PASS == kLinDx) {
+        plain_epilogue32<T>(a.out, row * a.N, a.N, c0, half, ok, v);
+    } else {
+        if (a.out_f32)
+            plain_epilogue32<float>(a.out, row * a.N, a.N, c0, half, ok, v);
+        else
+            plain_epilogue32<T>(a.out, row * a.N, a.N, c0, half, ok, v);
+    }
+}
+
+// ------------------------------------------------------------ tile list --
+// One output tile: rows m0 .. of the group's `rows` rows of C, the first of
+// them row row0 of the output; columns c0 ..; k from k0 to k1 (dW: rows of x
+// and dz).
+struct LinTile {
+    int g, part, m0, c0, rows, k0, k1;
+    int64_t row0;
+};
+
+// groups by rows, descending (ties by index): dW's tiles go longest first
+struct GroupOrder {
+    int by_rank[kMaxGroups];
+};
+__device__ __forceinline__ void order_groups(GroupOrder& o, const GroupWalk& w, int G) {
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+        const int n = w.off[g + 1] - w.off[g];
+        int rank = 0;
+        for (int q = 0; q < G; ++q) {
+            const int nq = w.off[q + 1] - w.off[q];
+            rank += (nq > n || (nq == n && q < g)) ? 1 : 0;
+        }
+        o.by_rank[rank] = g;
+    }
+    __syncthreads();
+}
+
+// Tiles go in supertiles of 4 x 4 within a group (n-blocks of four n-tiles,
+// within those m-blocks of four m-tiles): tiles that run at the same time
+// share operand panels in their XCD's L2.
+__device__ __forceinline__ void lin_supertile(int M, int N, int j, int& m, int& nt) {
+    const int nb = j / (4 * M);
+    const int w = min(4, N - 4 * nb);
+    const int r = j - nb * 4 * M;
+    const int mb = r / (4 * w);
+    const int hgt = min(4, M - 4 * mb);
+    const int rr = r - mb * 4 * w;
+    nt = 4 * nb + rr / hgt;
+    m = 4 * mb + rr % hgt;
+}
+
+// k range of part s of `parts` of k values k_lo .. k_hi: whole slices of 32
+__device__ __forceinline__ void part_range(int k_lo, int k_hi, int s, int parts, int& k0, int& k1) {
+    if (parts == 1) {
+        k0 = k_lo;
+        k1 = k_hi;
+        return;
+    }
+    const int slices = (k_hi - k_lo + 31) / 32;
+    const int per = (slices + parts - 1) / parts;
+    k0 = min(k_hi, k_lo + 32 * per * s);
+    k1 = min(k_hi, k0 + 32 * per);
+}
+
+// The position `i` of this work-group's list -> tile, or false past its end.
+// Forward and dx: the list of tiles (part by part, group by group) is cut into
+// eight equal runs, one for each XCD (work-groups b with b % 8 = x), dealt
+// round-robin to its work-groups: every m-tile takes equally long, and an
+// XCD's L2 sees few groups' weights. dW: tiles take as long as their group
+// has rows, so groups go longest first, and four tiles at a time to each XCD.
+template <int PASS, int BM, int BN>
+__device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w, const GroupOrder& o, int i,
+                                         LinTile& t) {
+    const int xcd = blockIdx.x & 7, per_xcd = gridDim.x >> 3;
+    const int c = static_cast<int>(blockIdx.x >> 3) + i * per_xcd;
+    if constexpr (PASS == kLinDw) {
+        const int per_group = a.mtiles * a.ntn;
+        const int total = a.G * per_group * a.parts;
+        const int L = ((c >> 2) * 8 + xcd) * 4 + (c & 3);
+        if (L >= total) return false;
+        const int gp = L / per_group;
+        const int rank = gp / a.parts;
+        t.part = gp - rank * a.parts;
+        t.g = __builtin_amdgcn_readfirstlane(o.by_rank[rank]);
+        int m, nt;
+        lin_supertile(a.mtiles, a.ntn, L - gp * per_group, m, nt);
+        t.m0 = m * BM;
+        t.c0 = nt * BN;
+        t.rows = a.M;
+        t.row0 = static_cast<int64_t>(t.g) * a.M;
+        part_range(w.off[t.g], w.off[t.g + 1], t.part, a.parts, t.k0, t.k1);
+    } else {
+        // (the launch bounds the list to 2^30 tiles)
+        const int per_part = __builtin_amdgcn_readfirstlane(w.pre[a.G]) * a.ntn, total = per_part * a.parts;
+        const auto eighth = [&](int x) { return (total >> 3) * x + ((total & 7) * x >> 3); };
+        const int L = eighth(xcd) + c;
+        if (L >= eighth(xcd + 1)) return false;
+        t.part = a.parts == 1 ? 0 : L / per_part;
+        const int l = L - t.part * per_part;
+        t.g = group_of(w, a.G, l / a.ntn);
+        int m, nt;
+        lin_supertile(w.pre[t.g + 1] - w.pre[t.g], a.ntn, l - w.pre[t.g] * a.ntn, m, nt);
+        t.m0 = m * BM;
+        t.c0 = nt * BN;
+        t.rows = w.off[t.g + 1] - w.off[t.g];
+        t.row0 = w.off[t.g];
+        part_range(0, a.K, t.part, a.parts, t.k0, t.k1);
+    }
+    // (the same for every lane by construction)
+    t.g = __builtin_amdgcn_readfirstlane(t.g);
+    t.part = __builtin_amdgcn_readfirstlane(t.part);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.c0 = __builtin_amdgcn_readfirstlane(t.c0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    t.k0 = __builtin_amdgcn_readfirstlane(t.k0);
+    t.k1 = __builtin_amdgcn_readfirstlane(t.k1);
+    t.row0 = static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(t.row0)))) |
+             (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(t.row0 >> 32))) << 32);
+    return true;
+}
+
+}  // namespace moe

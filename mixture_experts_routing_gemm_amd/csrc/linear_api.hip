@@ -1,0 +1,298 @@
+// Host side of the linear layer's and the rows8 format's C entry points
+// (include/moe.h): argument validation, workspace layout, the choice of tiles
+// and the launch sequence. No call here allocates or synchronises.
+#include <algorithm>
+
+#include "api_common.h"
+#include "linear.h"
+
+namespace moe {
+
+struct DzArgs {
+    const int32_t* offsets;
+    int64_t R;
+    int G, N, fn;
+    const uint8_t* dy;
+    const uint8_t* z;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t n32;
+    uint8_t* dz;
+    float* db_part;
+};
+
+int device_cus();
+hipError_t launch_linear_bf16(int pass, const LinearArgs& a, int shape, hipStream_t st);
+hipError_t launch_linear_f32(int pass, const LinearArgs& a, int shape, hipStream_t st);
+hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st);
+int64_t linear_db_tiles(int64_t R, int G);
+hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st);
+hipError_t launch_linear_db(const int32_t* offsets, int64_t R, int G, int N, const float* part, void* db, bool f32,
+                            hipStream_t st);
+hipError_t launch_pack_rows8(int64_t rows, int n, bool f32, const void* x, void* packed, hipStream_t st);
+hipError_t launch_unpack_rows8(int64_t rows, int n, bool f32, const void* packed, void* x, hipStream_t st);
+
+}  // namespace moe
+
+using namespace moe;
+
+namespace {
+
+int32_t check_linear(const moe_linear_shape* s, bool grouped) {
+    if (s == nullptr) return MOE_ERR_INVALID_ARG;
+    if (s->rows < 0 || s->n_in <= 0 || s->n_out <= 0 || s->groups <= 0 || s->fn < MOE_FN_NONE || s->fn > MOE_FN_SILU ||
+        s->save < MOE_SAVE_NONE || s->save > MOE_SAVE_INT8 || (!grouped && s->groups != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (s->act != MOE_F32 && s->act != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (s->grad != MOE_F32 && s->grad != s->act) return MOE_ERR_UNSUPPORTED;
+    const int unit = s->act == MOE_F32 ? 4 : 8;
+    if (s->rows >= (int64_t(1) << 31) || s->n_in > (1 << 20) || s->n_out > (1 << 20) || s->n_in % unit != 0 ||
+        s->n_out % unit != 0 || s->groups > kMaxGroups)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+size_t act_size(const moe_linear_shape& s) { return s.act == MOE_F32 ? 4 : 2; }
+
+size_t saved_size(const moe_linear_shape& s) {
+    if (s.save == MOE_SAVE_ACT) return align256(static_cast<size_t>(s.rows) * s.n_out * act_size(s));
+    if (s.save == MOE_SAVE_INT8) return rows8_bytes(s.rows, s.n_out);
+    return 0;
+}
+
+// How a product is run: its tile shape and in how many parts k is split.
+struct Plan {
+    int shape, parts;
+};
+Plan plan_of(const moe_linear_shape& s, int pass) {
+    Plan p{0, 1};
+    const int64_t avg = s.rows / s.groups;
+    if (s.act == MOE_F32) {
+        p.shape = pass == kLinDw ? (s.n_out >= 128 && s.n_in >= 128 ? 0 : 1) : (avg >= 96 ? 0 : 1);
+    } else if (pass == kLinDw) {
+        p.shape = s.n_out >= 256 && s.n_in >= 256 ? 0 : 1;
+    } else {
+        p.shape = avg >= 192 ? 0 : (avg >= 96 ? 1 : 2);
+    }
+    return p;
+}
+
+struct LinLayout {
+    size_t dz = 0, db = 0, part = 0, total = 0;
+};
+LinLayout linear_layout(const moe_linear_shape& s, bool backward) {
+    LinLayout L;
+    size_t off = kHeaderBytes;
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off = align256(off + n);
+        return at;
+    };
+    auto parts = [&](int pass, size_t rows, size_t n) {
+        const Plan p = plan_of(s, pass);
+        return p.parts > 1 ? p.parts * rows * n * 4 : 0;
+    };
+    const size_t R = static_cast<size_t>(s.rows), ni = s.n_in, no = s.n_out;
+    if (backward) {
+        L.dz = take(s.fn != MOE_FN_NONE ? R * no * act_size(s) : 0);
+        L.db = take(static_cast<size_t>(linear_db_tiles(s.rows, s.groups)) * no * 4);
+        L.part = take(std::max(parts(kLinDx, R, ni), parts(kLinDw, s.groups * no, ni)));
+    } else {
+        L.part = take(parts(kLinForward, R, no));
+    }
+    L.total = off;
+    return L;
+}
+
+int32_t check_linear_ws(size_t need, const void* ws, size_t ws_bytes) {
+    if (ws == nullptr || !aligned256(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+int32_t check_saved(const moe_linear_shape& s, const void* saved, size_t saved_bytes) {
+    if (s.save == MOE_SAVE_NONE) return MOE_OK;
+    if (saved == nullptr || !aligned256(saved) || saved_bytes < saved_size(s)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+hipError_t run_product(const moe_linear_shape& s, int pass, LinearArgs a, void* ws, size_t part_at, hipStream_t st) {
+    const Plan p = plan_of(s, pass);
+    const bool f32 = s.act == MOE_F32;
+    a.parts = p.parts;
+    a.part_out = p.parts > 1 ? at<float>(ws, part_at) : nullptr;
+    const hipError_t e = f32 ? launch_linear_f32(pass, a, p.shape, st) : launch_linear_bf16(pass, a, p.shape, st);
+    if (e != hipSuccess || p.parts == 1) return e;
+    return launch_linear_join(pass, a, f32, st);
+}
+
+int32_t linear_forward(const moe_linear_shape* s, const void* x, const int32_t* offsets, bool grouped, const void* w,
+                       const float* bias, const void* residual, void* y, void* saved, size_t saved_bytes, void* ws,
+                       size_t ws_bytes, void* stream) {
+    MOE_TRY(check_linear(s, grouped));
+    if (s->rows == 0) return MOE_OK;
+    MOE_TRY(check_ptrs({x, w, y}));
+    if (grouped) MOE_TRY(check_ptrs({offsets}));
+    MOE_TRY(check_opt({bias, residual}));
+    MOE_TRY(check_saved(*s, saved, saved_bytes));
+    const LinLayout L = linear_layout(*s, false);
+    MOE_TRY(check_linear_ws(L.total, ws, ws_bytes));
+    LinearArgs a{};
+    a.a = static_cast<const uint8_t*>(x);
+    a.b = static_cast<const uint8_t*>(w);
+    a.offsets = offsets;
+    a.hdr = static_cast<uint32_t*>(ws);
+    a.R = s->rows;
+    a.G = s->groups;
+    a.N = s->n_out;
+    a.K = s->n_in;
+    a.fn = s->fn;
+    a.bias = bias;
+    a.residual = static_cast<const uint8_t*>(residual);
+    a.out = static_cast<uint8_t*>(y);
+    if (s->save == MOE_SAVE_ACT) {
+        a.zsave = static_cast<uint8_t*>(saved);
+    } else if (s->save == MOE_SAVE_INT8) {
+        a.codes = static_cast<uint8_t*>(saved);
+        a.scales = a.codes + rows8_scales_at(s->rows, s->n_out);
+        a.n32 = rows8_stride(s->n_out);
+    }
+    return hip_status(run_product(*s, kLinForward, a, ws, L.part, static_cast<hipStream_t>(stream)));
+}
+
+int32_t linear_backward(const moe_linear_shape* s, const void* x, const int32_t* offsets, bool grouped, const void* w,
+                        const void* saved, size_t saved_bytes, const void* dy, void* dx, void* dw, void* db, void* ws,
+                        size_t ws_bytes, void* stream) {
+    MOE_TRY(check_linear(s, grouped));
+    if (s->fn != MOE_FN_NONE && s->save == MOE_SAVE_NONE) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_opt({x, w, dy, dx, dw, db, offsets}));
+    if (s->rows > 0) {
+        MOE_TRY(check_ptrs({dy}));
+        if (dx != nullptr) MOE_TRY(check_ptrs({w}));
+        if (dw != nullptr) MOE_TRY(check_ptrs({x}));
+        if (grouped) MOE_TRY(check_ptrs({offsets}));
+        if (s->fn != MOE_FN_NONE) MOE_TRY(check_saved(*s, saved, saved_bytes));
+    }
+    const LinLayout L = linear_layout(*s, true);
+    MOE_TRY(check_linear_ws(L.total, ws, ws_bytes));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool f32 = s->act == MOE_F32;
+    // (without rows the offsets are not read: every group is empty)
+    const int32_t* off = offsets;
+    const uint8_t* dz = static_cast<const uint8_t*>(dy);
+    if (s->rows > 0 && (s->fn != MOE_FN_NONE || db != nullptr)) {
+        DzArgs d{};
+        d.offsets = off;
+        d.R = s->rows;
+        d.G = s->groups;
+        d.N = s->n_out;
+        d.fn = s->fn;
+        d.dy = static_cast<const uint8_t*>(dy);
+        if (s->fn != MOE_FN_NONE) {
+            if (s->save == MOE_SAVE_ACT) {
+                d.z = static_cast<const uint8_t*>(saved);
+            } else {
+                d.codes = static_cast<const uint8_t*>(saved);
+                d.scales = d.codes + rows8_scales_at(s->rows, s->n_out);
+                d.n32 = rows8_stride(s->n_out);
+            }
+            d.dz = at<uint8_t>(ws, L.dz);
+            dz = d.dz;
+        }
+        d.db_part = db != nullptr ? at<float>(ws, L.db) : nullptr;
+        MOE_TRY(hip_status(launch_linear_dz(d, f32, st)));
+    }
+    LinearArgs a{};
+    a.a = dz;
+    a.offsets = off;
+    a.hdr = static_cast<uint32_t*>(ws);
+    a.R = s->rows;
+    a.G = s->groups;
+    a.fn = MOE_FN_NONE;
+    a.N = s->n_in;
+    if (dx != nullptr && s->rows > 0) {
+        a.b = static_cast<const uint8_t*>(w);
+        a.K = s->n_out;
+        a.out = static_cast<uint8_t*>(dx);
+        MOE_TRY(hip_status(run_product(*s, kLinDx, a, ws, L.part, st)));
+    }
+    if (dw != nullptr) {
+        a.b = static_cast<const uint8_t*>(x);
+        a.M = s->n_out;
+        a.K = 0;
+        a.out = static_cast<uint8_t*>(dw);
+        a.out_f32 = s->grad == MOE_F32 ? 1 : 0;
+        MOE_TRY(hip_status(run_product(*s, kLinDw, a, ws, L.part, st)));
+    }
+    if (db != nullptr)
+        MOE_TRY(hip_status(launch_linear_db(off, s->rows, s->groups, s->n_out, at<float>(ws, L.db), db,
+                                            s->grad == MOE_F32, st)));
+    return MOE_OK;
+}
+
+int32_t check_rows8(int64_t rows, int32_t n, int32_t dtype, const void* x, const void* packed, size_t bytes) {
+    if (rows < 0 || n < 1) return MOE_ERR_INVALID_ARG;
+    if (n > (1 << 20) || rows >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    MOE_TRY(check_ptrs({x, packed}));
+    if (!aligned256(packed) || bytes < rows8_bytes(rows, n)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_bytes(const moe_linear_shape* s, int32_t stage) {
+    if (check_linear(s, true) != MOE_OK) return 0;
+    if (stage != MOE_STAGE_LINEAR && stage != MOE_STAGE_LINEAR_BACKWARD) return 0;
+    return linear_layout(*s, stage == MOE_STAGE_LINEAR_BACKWARD).total;
+}
+
+size_t moe_linear_saved_bytes(const moe_linear_shape* s) {
+    return check_linear(s, true) == MOE_OK ? saved_size(*s) : 0;
+}
+
+int32_t moe_grouped_linear(const moe_linear_shape* s, const void* x, const int32_t* offsets, const void* w,
+                           const float* bias, const void* residual, void* y, void* saved, size_t saved_bytes, void* ws,
+                           size_t ws_bytes, void* stream) {
+    return linear_forward(s, x, offsets, true, w, bias, residual, y, saved, saved_bytes, ws, ws_bytes, stream);
+}
+
+int32_t moe_linear(const moe_linear_shape* s, const void* x, const void* w, const float* bias, const void* residual,
+                   void* y, void* saved, size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
+    return linear_forward(s, x, nullptr, false, w, bias, residual, y, saved, saved_bytes, ws, ws_bytes, stream);
+}
+
+int32_t moe_grouped_linear_backward(const moe_linear_shape* s, const void* x, const int32_t* offsets, const void* w,
+                                    const void* saved, size_t saved_bytes, const void* dy, void* dx, void* dw, void* db,
+                                    void* ws, size_t ws_bytes, void* stream) {
+    return linear_backward(s, x, offsets, true, w, saved, saved_bytes, dy, dx, dw, db, ws, ws_bytes, stream);
+}
+
+int32_t moe_linear_backward(const moe_linear_shape* s, const void* x, const void* w, const void* saved,
+                            size_t saved_bytes, const void* dy, void* dx, void* dw, void* db, void* ws, size_t ws_bytes,
+                            void* stream) {
+    return linear_backward(s, x, nullptr, false, w, saved, saved_bytes, dy, dx, dw, db, ws, ws_bytes, stream);
+}
+
+size_t moe_rows8_bytes(int64_t rows, int32_t n) {
+    if (rows < 0 || rows >= (int64_t(1) << 40) || n < 1 || n > (1 << 20)) return 0;
+    return rows8_bytes(rows, n);
+}
+
+int32_t moe_pack_rows8(int64_t rows, int32_t n, int32_t dtype, const void* x, void* packed, size_t packed_bytes,
+                       void* stream) {
+    MOE_TRY(check_rows8(rows, n, dtype, x, packed, packed_bytes));
+    if (rows == 0) return MOE_OK;
+    return hip_status(launch_pack_rows8(rows, n, dtype == MOE_F32, x, packed, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_unpack_rows8(int64_t rows, int32_t n, int32_t dtype, const void* packed, size_t packed_bytes, void* x,
+                         void* stream) {
+    MOE_TRY(check_rows8(rows, n, dtype, x, packed, packed_bytes));
+    if (rows == 0) return MOE_OK;
+    return hip_status(launch_unpack_rows8(rows, n, dtype == MOE_F32, packed, x, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+// The linear layer's kernels without a product: dz = dy fn'(zs) with the bias
+// gradient's partial sums, those sums joined, and the sums of a product that
+// was split along k joined (with the forward's epilogue, or as dx or dW).
+// All are bound by HBM.
+#include "linear.h"
+
+namespace moe {
+
+// rows a work-group sums into one partial of the bias gradient
+constexpr int kDzRows = 128;
+constexpr int kDzCols = 256;
+
+struct DzArgs {
+    const int32_t* offsets;
+    int64_t R;
+    int G, N, fn;
+    const uint8_t* dy;       // [R, N] (act)
+    const uint8_t* z;        // [R, N] (act) or NULL
+    const uint8_t* codes;    // [R, n32] or NULL
+    const uint8_t* scales;
+    int64_t n32;
+    uint8_t* dz;             // [R, N] (act) or NULL
+    float* db_part;          // [m-tiles of 128 rows][N] or NULL
+};
+
+// A work-group takes 128 rows of one group and 256 columns: eight rows of 32
+// lanes x 8 columns at a time. dz is rounded to the act type once (the
+// products that read it need that type); the bias gradient sums it before the
+// rounding, each thread its rows in order, then the eight threads of a column
+// in order: no atomics, the same bits every call.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs a) {
+    __shared__ GroupWalk walk;
+    __shared__ float sums[8][kDzCols];
+    walk_groups(walk, a.offsets, a.R, a.G, kDzRows, nullptr);
+    const int mt = blockIdx.x;
+    if (mt >= walk.pre[a.G]) return;
+    const int g = group_of(walk, a.G, mt);
+    const int m0 = (mt - walk.pre[g]) * kDzRows;
+    const int rows = min(kDzRows, walk.off[g + 1] - walk.off[g] - m0);
+    const int64_t row0 = walk.off[g] + m0;
+    const int cl = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
+    const int c = blockIdx.y * kDzCols + cl;
+    const int nv = min(8, max(0, a.N - c));
+    float s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] = 0.0f;
+    if (nv > 0) {
+#pragma unroll 4
+        for (int r = rl; r < rows; r += 8) {
+            const int64_t row = row0 + r;
+            float v[8], z[8];
+            load8<T>(a.dy, row * a.N + c, nv, v);
+            if (a.fn != MOE_FN_NONE) {
+                if (a.z != nullptr) {
+                    load8<T>(a.z, row * a.N + c, nv, z);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + row * a.n32 + c);
+                    const float step = rows8_step(a.scales[row * (a.n32 / kRows8Block) + c / kRows8Block]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        z[u] = rows8_value(w.x, u, step);
+                        z[4 + u] = rows8_value(w.y, u, step);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] *= lin_slope(a.fn, z[u]);
+                store8<T>(a.dz, row * a.N + c, nv, v);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s[u] += v[u];
+        }
+    }
+    if (a.db_part == nullptr) return;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sums[rl][cl + u] = s[u];
+    __syncthreads();
+    const int col = blockIdx.y * kDzCols + threadIdx.x;
+    if (col < a.N) {
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) t += sums[r][threadIdx.x];
+        a.db_part[static_cast<int64_t>(mt) * a.N + col] = t;
+    }
+}
+
+// db[g][n] = the sum of the group's partials, four threads a column (each
+// every fourth partial, in order), then the four in order.
+template <typename TOut>
+__global__ __launch_bounds__(256) void linear_db_kernel(const int32_t* __restrict__ offsets, int64_t R, int G, int N,
+                                                        const float* __restrict__ part, TOut* __restrict__ db) {
+    __shared__ GroupWalk walk;
+    __shared__ float sums[4][64];
+    walk_groups(walk, offsets, R, G, kDzRows, nullptr);
+    const int g = blockIdx.y, col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+    float s = 0.0f;
+    if (col < N)
+        for (int t = walk.pre[g] + q; t < walk.pre[g + 1]; t += 4) s += part[static_cast<int64_t>(t) * N + col];
+    sums[q][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (q == 0 && col < N) {
+        const float t = ((sums[0][threadIdx.x] + sums[1][threadIdx.x]) + sums[2][threadIdx.x]) + sums[3][threadIdx.x];
+        if constexpr (sizeof(TOut) == 4)
+            db[static_cast<int64_t>(g) * N + col] = t;
+        else
+            db[static_cast<int64_t>(g) * N + col] = f32_to_bf16(t);
+    }
+}
+
+// The parts' sums of 32 x 32 values a wave, added part by part, then stored as
+// the tile kernels store a block.
+template <typename T, int PASS>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
+    __shared__ GroupWalk walk;
+    if constexpr (PASS != kLinDw) walk_groups(walk, a.offsets, a.R, a.G, 1, a.hdr);
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
+    const int nblk = (a.N + 31) / 32;
+    const int64_t blk = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (blk >= (all + 31) / 32 * nblk) return;
+    const int c0 = static_cast<int>(blk % nblk) * 32;
+    const int64_t row = blk / nblk * 32 + (lane & 31);
+    bool ok = row < all;
+    int g = 0;
+    if constexpr (PASS != kLinDw) {
+        // (rows of no group are left as they are)
+        ok = ok && row >= walk.off[0] && row < walk.off[a.G];
+        if (PASS == kLinForward && a.bias != nullptr && ok) {
+            int lo = 0, hi = a.G - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (walk.off[mid] <= row) lo = mid;
+                else hi = mid - 1;
+            }
+            g = lo;
+        }
+    }
+    float v[2][8];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[p][u] = 0.0f;
+        const int c = c0 + 16 * p + 8 * half, nv = min(8, a.N - c);
+        if (ok && nv > 0) {
+            for (int s = 0; s < a.parts; ++s) {
+                float t[8];
+                load8<float>(reinterpret_cast<const uint8_t*>(a.part_out), (s * all + row) * a.N + c, nv, t);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[p][u] += t[u];
+            }
+        }
+    }
+    if constexpr (PASS == kLinForward) {
+        linear_epilogue32<T>(a, g, row, c0, half, ok, v);
+    } else if (PASS == kLinDw && a.out_f32) {
+        plain_epilogue32<float>(a.out, row * a.N, a.N, c0, half, ok, v);
+    } else {
+        plain_epilogue32<T>(a.out, row * a.N, a.N, c0, half, ok, v);
+    }
+}
+
+int64_t linear_db_tiles(int64_t R, int G) { return R / kDzRows + G; }
+
+hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st) {
+    const int64_t mt = linear_db_tiles(a.R, a.G);
+    if (mt >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(mt), (a.N + kDzCols - 1) / kDzCols);
+    if (f32)
+        linear_dz_kernel<float><<<grid, 256, 0, st>>>(a);
+    else
+        linear_dz_kernel<bf16_t><<<grid, 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_db(const int32_t* offsets, int64_t R, int G, int N, const float* part, void* db, bool f32,
+                            hipStream_t st) {
+    const dim3 grid((N + 63) / 64, G);
+    if (f32)
+        linear_db_kernel<float><<<grid, 256, 0, st>>>(offsets, R, G, N, part, static_cast<float*>(db));
+    else
+        linear_db_kernel<bf16_t><<<grid, 256, 0, st>>>(offsets, R, G, N, part, static_cast<bf16_t*>(db));
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st) {
+    const int64_t all = pass == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
+    const int64_t blocks = ((all + 31) / 32 * ((a.N + 31) / 32) + 3) / 4;
+    if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const unsigned n = static_cast<unsigned>(blocks);
+    if (pass == kLinForward) {
+        if (f32) linear_join_kernel<float, kLinForward><<<n, 256, 0, st>>>(a);
+        else linear_join_kernel<bf16_t, kLinForward><<<n, 256, 0, st>>>(a);
+    } else if (pass == kLinDx) {
+        if (f32) linear_join_kernel<float, kLinDx><<<n, 256, 0, st>>>(a);
+        else linear_join_kernel<bf16_t, kLinDx><<<n, 256, 0, st>>>(a);
+    } else {
+        if (f32) linear_join_kernel<float, kLinDw><<<n, 256, 0, st>>>(a);
+        else linear_join_kernel<bf16_t, kLinDw><<<n, 256, 0, st>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_common.h"
 #include "ffn_plan.h"
 #include "moe.h"
 #include "moe_device.h"
@@ -89,17 +90,12 @@ static __device__ __align__(256) uint8_t scratch[kNoAllocScratchBytes];
 
 namespace {
 
-constexpr size_t kHeaderBytes = 256;
 // kernels of moe_forward_fp8w, in order: gate_topk, dispatch_rank,
 // dispatch_scan, dispatch_permute_fp8, ffn_plan, ffn_up, ffn_hidden_quant,
 // ffn_down, combine
 constexpr int kFp8wKernels = 9;
 
-size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-
 size_t act_bytes(int32_t dt) { return dt == MOE_F32 ? 4 : (dt == MOE_BF16 ? 2 : 1); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Layout {
     size_t x8 = 0, q8 = 0, h8_r = 0, h8_s = 0, hsc_r = 0, hsc_s = 0;  // fp8-weight forward
@@ -196,18 +192,6 @@ bool f8w_shape_ok(const moe_shape& s) {
            (s.quant == MOE_QUANT_TOKEN || s.quant == MOE_QUANT_TOKEN_ABSMAX) && f8w_supported(s);
 }
 
-int32_t check_ptrs(std::initializer_list<const void*> required) {
-    for (const void* p : required)
-        if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
-int32_t check_opt(std::initializer_list<const void*> optional) {
-    for (const void* p : optional)
-        if (p != nullptr && !aligned16(p)) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
 int32_t check_ws(const moe_shape& s, int stage, const void* ws, size_t ws_bytes) {
     const size_t need = layout(s, stage).total;
     if (need == 0) return MOE_OK;
@@ -215,19 +199,6 @@ int32_t check_ws(const moe_shape& s, int stage, const void* ws, size_t ws_bytes)
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     return MOE_OK;
 }
-
-int32_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-template <typename T>
-T* at(void* ws, size_t off) {
-    return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
-#define MOE_TRY(expr)                       \
-    do {                                    \
-        const int32_t _rc = (expr);         \
-        if (_rc != MOE_OK) return _rc;      \
-    } while (0)
 
 int32_t forward_impl(const moe_shape* s, const void* x, const void* w_gate, const float* bias,
                      const void* w1, const void* w3, const void* w2, void* y, int32_t* topk_idx,
@@ -365,7 +336,7 @@ const char* moe_status_string(int32_t status) {
         case MOE_ERR_UNSUPPORTED: return "unsupported shape or dtype combination";
         case MOE_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case MOE_ERR_HIP: return "HIP runtime error";
-        case MOE_ERR_BAD_INDEX: return "bad or repeated expert id in topk_idx";
+        case MOE_ERR_BAD_INDEX: return "bad or repeated expert id in topk_idx, or bad row offsets";
         default: return "unknown status";
     }
 }
