@@ -394,6 +394,43 @@ int32_t moe_grouped_ffn_backward_saved(const moe_shape *s, const void *x_perm,
                                        void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * The same with the activations kept in 8 bits: a third of the memory, and a
+ * backward that reads a third as much. The forward keeps a and b (quantised
+ * from their float32 sums, in the rows8 format of moe_pack_rows8); the
+ * backward takes the values read back, a' and b', in their place everywhere:
+ * hid' = silu(a') b' for dW2, da = dhid b' silu'(a'), db = dhid silu(a').
+ * The forward's results are moe_grouped_ffn's, bit for bit.
+ *
+ * moe_ffn_saved8_bytes: bytes of the buffer, or 0 when the shape is not
+ *  supported: act must be MOE_BF16, the shape on the persistent tiles
+ *  (d % 256 == 0, h % 128 == 0), and x, the weights W1 with W3 and the hidden
+ *  rows' gradients [rows, 2h] each below 4 GiB. The buffer holds four rows8
+ *  buffers: a and b of the routed rows [T*k, h], a and b of the shared
+ *  experts' token rows [T, S*h] (nothing for S = 0).
+ * moe_grouped_ffn_save8: moe_grouped_ffn (same arguments and results) that
+ *  also writes a and b into `saved8` (caller-owned, 256-byte aligned).
+ * moe_grouped_ffn_backward_saved8: as moe_grouped_ffn_backward, from
+ *  `saved8`; dw1, dw3, dw2 are of type `grad`, MOE_F32 or MOE_BF16 (summed in
+ *  float32 and rounded once). ws: MOE_STAGE_FFN_BACKWARD bytes. T = 0 only
+ *  zeroes the weight gradients.
+ * Errors as for moe_grouped_ffn_save and moe_grouped_ffn_backward_saved;
+ * MOE_ERR_UNSUPPORTED for another `grad`.
+ */
+size_t moe_ffn_saved8_bytes(const moe_shape *s);
+int32_t moe_grouped_ffn_save8(const moe_shape *s, const void *x_perm, const float *qparams,
+                              const int32_t *offsets, const void *x, const void *w1,
+                              const void *w3, const void *w2, void *y_perm, void *y_shared,
+                              void *saved8, size_t saved8_bytes, void *ws, size_t ws_bytes,
+                              void *stream);
+int32_t moe_grouped_ffn_backward_saved8(const moe_shape *s, const void *x_perm,
+                                        const float *qparams, const int32_t *offsets,
+                                        const void *x, const void *w1, const void *w3,
+                                        const void *w2, const void *saved8, size_t saved8_bytes,
+                                        const void *dy_perm, const void *dy_shared, void *dx_perm,
+                                        void *dx_shared, int32_t grad, void *dw1, void *dw3,
+                                        void *dw2, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * The whole layer: moe_gate_topk -> moe_dispatch -> moe_grouped_ffn ->
  * moe_combine with intermediates in the workspace (MOE_STAGE_FORWARD bytes).
  * y [T,d] (act) is the layer output; topk_idx, topk_w, counts, offsets,

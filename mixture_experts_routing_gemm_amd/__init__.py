@@ -24,6 +24,7 @@ from ._binding import (  # noqa: F401
     STAGE_LINEAR, STAGE_LINEAR_BACKWARD, alloc_linear_saved, alloc_linear_workspace, alloc_rows8,
     make_linear_shape, moe_grouped_linear, moe_grouped_linear_backward, moe_linear, moe_linear_backward,
     moe_linear_saved_bytes, moe_linear_shape, moe_linear_workspace_bytes, moe_pack_rows8, moe_rows8_bytes,
-    moe_unpack_rows8, moe_workspace_bytes,
+    moe_unpack_rows8, moe_ffn_saved8_bytes, alloc_saved8, moe_grouped_ffn_save8,
+    moe_grouped_ffn_backward_saved8, moe_workspace_bytes,
     moe_workspace_init, shape_of, status_string)
 from .buffers import ForwardBuffers  # noqa: F401

@@ -162,6 +162,13 @@ def _load():
     L.moe_forward_kernel_count.restype = i32
     L.moe_forward_kernel_name.argtypes = [sp, i32]
     L.moe_forward_kernel_name.restype = ctypes.c_char_p
+    L.moe_ffn_saved8_bytes.argtypes = [sp]
+    L.moe_ffn_saved8_bytes.restype = sz
+    L.moe_grouped_ffn_save8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp]
+    L.moe_grouped_ffn_save8.restype = i32
+    L.moe_grouped_ffn_backward_saved8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp,
+                                                  i32, vp, vp, vp, vp, sz, vp]
+    L.moe_grouped_ffn_backward_saved8.restype = i32
     lp, i64 = ctypes.POINTER(moe_linear_shape), ctypes.c_int64
     L.moe_linear_workspace_bytes.argtypes = [lp, i32]
     L.moe_linear_workspace_bytes.restype = sz
@@ -196,7 +203,8 @@ EXPORTS = ["moe_workspace_bytes", "moe_workspace_init", "moe_status_string", "mo
            "moe_ffn_saved_bytes", "moe_grouped_ffn_save", "moe_grouped_ffn_backward_saved",
            "moe_linear_workspace_bytes", "moe_linear_saved_bytes", "moe_grouped_linear", "moe_linear",
            "moe_grouped_linear_backward", "moe_linear_backward", "moe_rows8_bytes", "moe_pack_rows8",
-           "moe_unpack_rows8"]
+           "moe_unpack_rows8", "moe_ffn_saved8_bytes", "moe_grouped_ffn_save8",
+           "moe_grouped_ffn_backward_saved8"]
 
 
 def status_string(status: int) -> str:
@@ -530,3 +538,40 @@ def moe_unpack_rows8(packed, x, stream=None):
     rows, n, code = _rows8(x)
     pp, pn = _ws(packed)
     _check(lib.moe_unpack_rows8(rows, n, code, pp, pn, _p(x), _s(stream)), "moe_unpack_rows8")
+
+
+def moe_ffn_saved8_bytes(shape) -> int:
+    return int(lib.moe_ffn_saved8_bytes(ctypes.byref(shape)))
+
+
+def alloc_saved8(shape, device="cuda"):
+    """The caller buffer of a and b saved in 8 bits for the backward (uint8)."""
+    n = moe_ffn_saved8_bytes(shape)
+    if n == 0 and shape.T != 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_ffn_saved8_bytes: shape not supported")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_grouped_ffn_save8(shape, x_perm, qparams, offsets, x, w1, w3, w2, y_perm, y_shared, saved8, ws,
+                          stream=None):
+    wp, wn = _ws(ws)
+    sv, sn = _ws(saved8)
+    _check(lib.moe_grouped_ffn_save8(ctypes.byref(shape), _p(x_perm), _p(qparams), _p(offsets), _p(x),
+                                     _p(w1), _p(w3), _p(w2), _p(y_perm), _p(y_shared), sv, sn, wp, wn,
+                                     _s(stream)), "moe_grouped_ffn_save8")
+
+
+def moe_grouped_ffn_backward_saved8(shape, x_perm, qparams, offsets, x, w1, w3, w2, saved8, dy_perm,
+                                    dy_shared, dx_perm, dx_shared, grad, dw1, dw3, dw2, ws, stream=None):
+    """grad: the type of dw1, dw3 and dw2, "f32" or "bf16"."""
+    wp, wn = _ws(ws)
+    sv, sn = _ws(saved8)
+    g = _DTYPES[grad] if isinstance(grad, str) else int(grad)
+    n = (shape.E + shape.S) * shape.d * shape.h
+    if g not in _TORCH:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_grouped_ffn_backward_saved8: grad")
+    _check(lib.moe_grouped_ffn_backward_saved8(
+        ctypes.byref(shape), _p(x_perm), _p(qparams), _p(offsets), _p(x), _p(w1), _p(w3), _p(w2), sv, sn,
+        _p(dy_perm), _p(dy_shared), _p(dx_perm), _p(dx_shared), g, _t(dw1, _TORCH[g], n, "dw1"),
+        _t(dw3, _TORCH[g], n, "dw3"), _t(dw2, _TORCH[g], n, "dw2"), wp, wn, _s(stream)),
+        "moe_grouped_ffn_backward_saved8")

@@ -72,9 +72,10 @@ struct BwdArgs {
     uint8_t* db_s;
     uint8_t* dx_perm;        // [R, d]
     uint8_t* dx_sh;          // [T, d]
-    float* dw1;              // [G, h, d]
-    float* dw3;              // [G, h, d]
-    float* dw2;              // [G, d, h]
+    void* dw1;               // [G, h, d], float32, or bf16 with dw_bf16
+    void* dw3;               // [G, h, d]
+    void* dw2;               // [G, d, h]
+    int dw_bf16;
     int ntn;                 // n-tiles per group (dh, dx)
     int tpg;                 // output tiles per group and gradient (wgrad)
     // layout of the da / db rows the weight gradients read: row stride of a
@@ -446,7 +447,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ffn_bwd_wgrad_kernel(BwdArgs a
 
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1, lr = lane & 31, lg = lane >> 5;
-    float* out = (q == 0 ? a.dw2 : (q == 1 ? a.dw1 : a.dw3)) + static_cast<int64_t>(g) * M * N;
+    void* const dw = q == 0 ? a.dw2 : (q == 1 ? a.dw1 : a.dw3);
+    float* out = static_cast<float*>(dw) + static_cast<int64_t>(g) * M * N;
+    bf16_t* out16 = static_cast<bf16_t*>(dw) + static_cast<int64_t>(g) * M * N;
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
@@ -456,7 +459,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ffn_bwd_wgrad_kernel(BwdArgs a
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
                 const int n = n0 + wn * 64 + nb * 32 + lr;
-                if (n < N) out[static_cast<int64_t>(m) * N + n] = acc[mb][nb][v];
+                if (n >= N) continue;
+                if (a.dw_bf16) out16[static_cast<int64_t>(m) * N + n] = f32_to_bf16(acc[mb][nb][v]);
+                else out[static_cast<int64_t>(m) * N + n] = acc[mb][nb][v];
             }
         }
 }
@@ -510,13 +515,13 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
                                 const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh,
                                 int32_t* plan_f, int32_t* plan_dh, void* h_r, void* h_s, void* a_r,
                                 void* b_r, void* a_s, void* b_s, void* dd_r, void* dd_s,
-                                hipStream_t st, const Marks* mk, bool recompute);
+                                hipStream_t st, const Marks* mk, bool recompute, const void* saved8);
 bool wgrad_supported(const moe_shape& s);
 size_t wgrad_ws_bytes(const moe_shape& s);
 hipError_t launch_ffn_wgrad(const moe_shape& s, const int32_t* offsets, const void* dd_r,
                             const void* dd_s, const void* v_r, const void* v_s, const void* dy_r,
-                            const void* dy_s, const void* hid_r, const void* hid_s, float* dw1,
-                            float* dw3, float* dw2, void* ws, hipStream_t st);
+                            const void* dy_s, const void* hid_r, const void* hid_s, void* dw1,
+                            void* dw3, void* dw2, bool bf16, void* ws, hipStream_t st);
 hipError_t launch_ffn_plan128(const moe_shape& s, const int32_t* offsets, int32_t* plan,
                               hipStream_t st);
 hipError_t launch_ffn_recompute(const moe_shape& s, const void* x_perm, const float* qparams,
@@ -606,10 +611,14 @@ SavedLayout saved_layout(const moe_shape& s) {
 hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const float* qparams,
                                const int32_t* offsets, const void* x, const void* w1,
                                const void* w3, const void* w2, const void* dy_perm,
-                               const void* dy_sh, void* dx_perm, void* dx_sh, float* dw1,
-                               float* dw3, float* dw2, void* ws, hipStream_t st,
-                               const Marks* mk, const void* saved) {
+                               const void* dy_sh, void* dx_perm, void* dx_sh, void* dw1,
+                               void* dw3, void* dw2, void* ws, hipStream_t st,
+                               const Marks* mk, const void* saved, const void* saved8,
+                               bool dw_bf16) {
     const BwdLayout L = bwd_layout(s);
+    // (a and b in 8 bits: the dh kernel of the persistent path reads them and
+    // writes hid into the workspace)
+    if (saved8 != nullptr && !L.big) return hipErrorInvalidValue;
     uint8_t* w = static_cast<uint8_t*>(ws);
     // a, b and hid: saved by the forward, or recomputed into the workspace
     const SavedLayout SL = saved_layout(s);
@@ -652,6 +661,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
     a.dw1 = dw1;
     a.dw3 = dw3;
     a.dw2 = dw2;
+    a.dw_bf16 = dw_bf16 ? 1 : 0;
     hipError_t e;
     mark(mk);
     if (L.big) {
@@ -671,7 +681,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
                                  dx_perm, dx_sh, reinterpret_cast<int32_t*>(w + L.plan),
                                  reinterpret_cast<int32_t*>(w + L.plan_dh), p_h_r, p_h_s,
                                  p_a_r, p_b_r, p_a_s, p_b_s, w + L.da_r, w + L.da_s,
-                                 st, mk, sv == nullptr);
+                                 st, mk, sv == nullptr && saved8 == nullptr, saved8);
         if (e != hipSuccess) return e;
         // the weight gradients read [da | db] rows and the routed m-tile
         // prefix of 128-row tiles is not needed by them
@@ -706,7 +716,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
     }
     if (L.big && L.wg) {
         e = launch_ffn_wgrad(s, offsets, w + L.da_r, w + L.da_s, x_perm, x, dy_perm, dy_sh, p_h_r,
-                             p_h_s, dw1, dw3, dw2, w + L.wgq, st);
+                             p_h_s, dw1, dw3, dw2, dw_bf16, w + L.wgq, st);
         if (e != hipSuccess) return e;
         mark(mk);
         return hipSuccess;

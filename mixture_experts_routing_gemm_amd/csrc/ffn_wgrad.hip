@@ -54,9 +54,9 @@ struct WgradArgs {
     // hidden rows: routed [R, h], shared [T, S*h]
     const uint8_t* hid_r;
     const uint8_t* hid_s;
-    float* dw1;  // [G, h, d]
-    float* dw3;  // [G, h, d]
-    float* dw2;  // [G, d, h]
+    void* dw1;  // [G, h, d], float32 or bf16
+    void* dw3;  // [G, h, d]
+    void* dw2;  // [G, d, h]
     uint32_t bytes_dd_r, bytes_dd_s, bytes_v_r, bytes_v_s, bytes_dy_r, bytes_dy_s, bytes_hid_r,
         bytes_hid_s;
     int ntiles;  // tiles per group: t13 [dW1; dW3] tiles, then the dW2 ones
@@ -180,8 +180,13 @@ __device__ __forceinline__ WgTile wg_decode(const WgradArgs& a, int L) {
     return t;
 }
 
+// TOut: float, or bf16_t (each sum rounded once)
+template <typename TOut>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_wgrad_kernel(WgradArgs a) {
+    TOut* const dw1 = static_cast<TOut*>(a.dw1);
+    TOut* const dw3 = static_cast<TOut*>(a.dw3);
+    TOut* const dw2 = static_cast<TOut*>(a.dw2);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     int* lds_next = reinterpret_cast<int*>(lds + kWgLds);
     const int tid = threadIdx.x;
@@ -212,16 +217,17 @@ void ffn_wgrad_kernel(WgradArgs a) {
             // 64 lanes instead of through the accumulator layout
             const int M0 = t.mt * kWgT, N0 = t.nt * kWgT;
             const int ncols = t.type == 0 ? kWgT : min(kWgT, a.h - N0);
-            const int q = ncols / 4;  // 16-byte chunks a row
+            constexpr int per = 16 / sizeof(TOut);
+            const int q = ncols / per;  // 16-byte chunks a row
             for (int i = tid; i < kWgT * q; i += 512) {
-                const int m = M0 + i / q, col = N0 + 4 * (i % q);
-                float* out;
+                const int m = M0 + i / q, col = N0 + per * (i % q);
+                TOut* out;
                 if (t.type == 0)
-                    out = m < a.h ? a.dw1 + (static_cast<int64_t>(t.g) * a.h + m) * a.d + col
-                                  : a.dw3 + (static_cast<int64_t>(t.g) * a.h + (m - a.h)) * a.d + col;
+                    out = m < a.h ? dw1 + (static_cast<int64_t>(t.g) * a.h + m) * a.d + col
+                                  : dw3 + (static_cast<int64_t>(t.g) * a.h + (m - a.h)) * a.d + col;
                 else
-                    out = a.dw2 + (static_cast<int64_t>(t.g) * a.d + m) * a.h + col;
-                *reinterpret_cast<f32x4*>(out) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    out = dw2 + (static_cast<int64_t>(t.g) * a.d + m) * a.h + col;
+                store16(out, u32x4{0u, 0u, 0u, 0u});
             }
             wait_vmcnt<0>();
             __syncthreads();
@@ -363,14 +369,14 @@ void ffn_wgrad_kernel(WgradArgs a) {
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
             const int mblk = M0 + wm * 128 + mb * 32;  // 32 rows, all in dW1, dW3 or dW2
-            float* out;
+            TOut* out;
             int ldo;
             if (t.type == 0) {
-                out = mblk < a.h ? a.dw1 + (static_cast<int64_t>(t.g) * a.h + mblk) * a.d
-                                 : a.dw3 + (static_cast<int64_t>(t.g) * a.h + (mblk - a.h)) * a.d;
+                out = mblk < a.h ? dw1 + (static_cast<int64_t>(t.g) * a.h + mblk) * a.d
+                                 : dw3 + (static_cast<int64_t>(t.g) * a.h + (mblk - a.h)) * a.d;
                 ldo = a.d;
             } else {
-                out = a.dw2 + (static_cast<int64_t>(t.g) * a.d + mblk) * a.h;
+                out = dw2 + (static_cast<int64_t>(t.g) * a.d + mblk) * a.h;
                 ldo = a.h;
             }
 #pragma unroll
@@ -380,7 +386,10 @@ void ffn_wgrad_kernel(WgradArgs a) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int m = 8 * (v >> 2) + 4 * lg + (v & 3);
-                    out[static_cast<int64_t>(m) * ldo + n + lr] = acc[mb][nb][v];
+                    if constexpr (sizeof(TOut) == 4)
+                        out[static_cast<int64_t>(m) * ldo + n + lr] = acc[mb][nb][v];
+                    else
+                        out[static_cast<int64_t>(m) * ldo + n + lr] = f32_to_bf16(acc[mb][nb][v]);
                 }
             }
         }
@@ -405,15 +414,21 @@ size_t wgrad_ws_bytes(const moe_shape& s) { return static_cast<size_t>(s.E + s.S
 
 int device_cus();
 
+template <typename TOut>
+hipError_t allow_wgrad_lds() {
+    static hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_wgrad_kernel<TOut>),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, kWgLds + 16);
+    return err;
+}
+
 // ws: wgrad_ws_bytes(s) (the group order and the queue). [da | db] rows as the
 // backward's persistent path writes them.
 hipError_t launch_ffn_wgrad(const moe_shape& s, const int32_t* offsets, const void* dd_r,
                             const void* dd_s, const void* v_r, const void* v_s, const void* dy_r,
-                            const void* dy_s, const void* hid_r, const void* hid_s, float* dw1,
-                            float* dw3, float* dw2, void* ws, hipStream_t st) {
-    static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_wgrad_kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kWgLds + 16);
+                            const void* dy_s, const void* hid_r, const void* hid_s, void* dw1,
+                            void* dw3, void* dw2, bool bf16, void* ws, hipStream_t st) {
     static_assert(kWgLds + 16 <= 160 * 1024, "LDS");
+    const hipError_t attr = bf16 ? allow_wgrad_lds<bf16_t>() : allow_wgrad_lds<float>();
     if (attr != hipSuccess) return attr;
     const int G = s.E + s.S;
     int32_t* order = static_cast<int32_t*>(ws);
@@ -454,7 +469,10 @@ hipError_t launch_ffn_wgrad(const moe_shape& s, const int32_t* offsets, const vo
     a.ntiles = ntiles;
     // a multiple of 8 work-groups (one per CU): the same count on every XCD
     const unsigned blocks = static_cast<unsigned>(std::max(8, device_cus() & ~7));
-    ffn_wgrad_kernel<<<blocks, 512, kWgLds + 16, st>>>(a);
+    if (bf16)
+        ffn_wgrad_kernel<bf16_t><<<blocks, 512, kWgLds + 16, st>>>(a);
+    else
+        ffn_wgrad_kernel<float><<<blocks, 512, kWgLds + 16, st>>>(a);
     return hipGetLastError();
 }
 
@@ -467,8 +485,7 @@ hipError_t launch_ffn_wgrad(const moe_shape& s, const int32_t* offsets, const vo
 hipError_t launch_wgrad_planes(const int32_t* offsets, int C, int64_t T, int d, int F,
                                const void* zp, const void* x, float* p1, float* p3, void* ws,
                                hipStream_t st) {
-    static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&ffn_wgrad_kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kWgLds + 16);
+    const hipError_t attr = allow_wgrad_lds<float>();
     if (attr != hipSuccess) return attr;
     if (C < 1 || C > kMaxE || F % kWgT != 0 || d % kWgT != 0) return hipErrorInvalidValue;
     int32_t* order = static_cast<int32_t*>(ws);
@@ -492,7 +509,7 @@ hipError_t launch_wgrad_planes(const int32_t* offsets, int C, int64_t T, int d, 
     a.t13 = (F / kWgT) * (d / kWgT);
     a.ntiles = a.t13;
     const unsigned blocks = static_cast<unsigned>(std::max(8, device_cus() & ~7));
-    ffn_wgrad_kernel<<<blocks, 512, kWgLds + 16, st>>>(a);
+    ffn_wgrad_kernel<float><<<blocks, 512, kWgLds + 16, st>>>(a);
     return hipGetLastError();
 }
 

@@ -24,6 +24,7 @@
 
 #include "ffn_plan.h"
 #include "lds_ring.h"
+#include "linear.h"
 #include "moe_device.h"
 
 namespace moe {
@@ -35,12 +36,18 @@ namespace moe {
 // kModeUp / kModeUpFp8 that also store the pre-activations a and b;
 // kModeDh computes dhid = dy W2 (K = d, from the transposed W2, one weight
 // row per output column) with the SwiGLU backward in its epilogue.
+// kModeUpSave8, kModeUpFp8Save8 and kModeDh8 are the same with a and b kept in
+// 8 bits (rows8.h); kModeDh8 also writes the hidden rows again, from the a and
+// b that it reads, for the weight gradient of W2.
 enum {
     kModeUp = 0, kModeUpFp8 = 1, kModeDown = 2, kModeUpF8W = 3, kModeDownF8W = 4,
-    kModeUpSave = 5, kModeUpFp8Save = 6, kModeDh = 7
+    kModeUpSave = 5, kModeUpFp8Save = 6, kModeDh = 7, kModeUpSave8 = 8, kModeUpFp8Save8 = 9,
+    kModeDh8 = 10
 };
 constexpr bool is_down(int m) { return m == kModeDown || m == kModeDownF8W; }
-constexpr bool is_fp8rows(int m) { return m == kModeUpFp8 || m == kModeUpFp8Save; }
+constexpr bool is_fp8rows(int m) { return m == kModeUpFp8 || m == kModeUpFp8Save || m == kModeUpFp8Save8; }
+constexpr bool is_save8(int m) { return m == kModeUpSave8 || m == kModeUpFp8Save8; }
+constexpr bool is_dh(int m) { return m == kModeDh || m == kModeDh8; }
 constexpr bool is_save(int m) { return m == kModeUpSave || m == kModeUpFp8Save; }
 constexpr bool is_f8w(int m) { return m == kModeUpF8W || m == kModeDownF8W; }
 // bf16 operands in both roles: the upper row of waves (0-3) issues every
@@ -89,6 +96,14 @@ struct GemmArgs {
     uint8_t* pre_b_routed;
     uint8_t* pre_a_shared;
     uint8_t* pre_b_shared;
+    // the 8-bit modes: pre_* are then codes, and these their scale bytes, a row
+    // of h / 32 (routed) or S h / 32 (shared); dh: the hidden rows, laid out as H
+    uint8_t* sc_a_routed;
+    uint8_t* sc_b_routed;
+    uint8_t* sc_a_shared;
+    uint8_t* sc_b_shared;
+    uint8_t* hid_routed;
+    uint8_t* hid_shared;
     // fp8-weight modes: (scale, centre) of the shared experts' token rows
     // [T, 2]; the weight scales s1 | qsum1 | s3 | qsum3 [G, h] | s2 [G, d];
     // the hidden rows' scales, routed [rows] and shared [T]
@@ -586,7 +601,7 @@ __device__ __forceinline__ void tile_sources(const GemmArgs& a, const TileInfo& 
             if (is_down(MODE)) {
                 const int n = ti.nt * kBigBN + br;
                 out[i] = static_cast<uint32_t>(n) * a.h * eb + c * 16;
-            } else if (MODE == kModeDh) {
+            } else if (is_dh(MODE)) {
                 // the transposed W2 [G, h, d]: weight row n is hidden feature n
                 // (rows past h, in a last partial n-tile, are read and unused)
                 const int n = ti.nt * kBigBN + br;
@@ -1154,7 +1169,35 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                 }
             }
         };
+        // dh from 8 bits: the codes of the same values, a word of four, and the
+        // step of each 32-value block (a block is the 32 columns of one nb)
+        uint32_t dh_cd[NB][4][2];
+        float dh_st[NB][2];
+        auto dh_load8 = [&](int mbi) {
+            const int rr = cur.m0 + wm * kBigWM + mbi * 32 + lr;
+            const int sg = cur.shared ? cur.g - a.E : 0;
+            const int lpre = cur.shared ? a.S * a.h : a.h;
+            const int64_t prow = static_cast<int64_t>(cur.row_base) + min(rr, cur.nrows - 1);
+            const uint8_t* ca = (cur.shared ? a.pre_a_shared : a.pre_a_routed) + prow * lpre + sg * a.h;
+            const uint8_t* cb = (cur.shared ? a.pre_b_shared : a.pre_b_routed) + prow * lpre + sg * a.h;
+            const uint8_t* sa = (cur.shared ? a.sc_a_shared : a.sc_a_routed) + (prow * lpre + sg * a.h) / kRows8Block;
+            const uint8_t* sb = (cur.shared ? a.sc_b_shared : a.sc_b_routed) + (prow * lpre + sg * a.h) / kRows8Block;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int col = cur.nt * kBigBN + wn * kBigWN + nb * 32;
+                const bool in = col < a.h;
+                dh_st[nb][0] = rows8_step(in ? sa[col / kRows8Block] : 0u);
+                dh_st[nb][1] = rows8_step(in ? sb[col / kRows8Block] : 0u);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int f = col + 8 * q + 4 * lg;
+                    dh_cd[nb][q][0] = in ? *reinterpret_cast<const uint32_t*>(ca + f) : 0u;
+                    dh_cd[nb][q][1] = in ? *reinterpret_cast<const uint32_t*>(cb + f) : 0u;
+                }
+            }
+        };
         if constexpr (MODE == kModeDh) dh_load(0, 0);
+        if constexpr (MODE == kModeDh8) dh_load8(0);
         if constexpr (kStage) {
             ring_barrier();
             stage = lds + 3 * kBigSlot + wave * 4096;
@@ -1221,7 +1264,7 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                         __builtin_amdgcn_raw_buffer_store_b128(
                             v[i], orsrc, obase + static_cast<uint32_t>(mb * 32 + 8 * i) * orow, 0, 2);
                 }
-            } else if constexpr (MODE == kModeDh) {
+            } else if constexpr (is_dh(MODE)) {
                 // dhid -> da = dhid b s (1 + a (1 - s)), db = dhid silu(a)
                 // (s = sigmoid(a)) from the recomputed a, b; da and db of a
                 // group's row side by side: [da | db], 2h values per group
@@ -1229,18 +1272,32 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                 const int lpre = cur.shared ? a.S * a.h : a.h;
                 const int lout = 2 * lpre;
                 const int cb = 0;
-                if (mb > 0) dh_load(mb, 0);
+                if (mb > 0) {
+                    if constexpr (MODE == kModeDh8) dh_load8(mb);
+                    else dh_load(mb, 0);
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     const int col = cur.nt * kBigBN + wn * kBigWN + nb * 32;
                     if (col >= a.h) continue;  // a last partial n-tile (h % 256 == 128)
-                    uint32_t wa_[4][2], wb_[4][2];
+                    uint32_t wa_[4][2], wb_[4][2], wh_[4][2];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint2 av4 = dh_ab[cb][nb][q][0];
-                        const uint2 bv4 = dh_ab[cb][nb][q][1];
-                        const float av[4] = {bf16_lo(av4.x), bf16_hi(av4.x), bf16_lo(av4.y), bf16_hi(av4.y)};
-                        const float bv[4] = {bf16_lo(bv4.x), bf16_hi(bv4.x), bf16_lo(bv4.y), bf16_hi(bv4.y)};
+                        float av[4], bv[4];
+                        if constexpr (MODE == kModeDh8) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                av[u] = rows8_value(dh_cd[nb][q][0], u, dh_st[nb][0]);
+                                bv[u] = rows8_value(dh_cd[nb][q][1], u, dh_st[nb][1]);
+                            }
+                            wh_[q][0] = pack_bf16x2(silu(av[0]) * bv[0], silu(av[1]) * bv[1]);
+                            wh_[q][1] = pack_bf16x2(silu(av[2]) * bv[2], silu(av[3]) * bv[3]);
+                        } else {
+                            const uint2 av4 = dh_ab[cb][nb][q][0];
+                            const uint2 bv4 = dh_ab[cb][nb][q][1];
+                            av[0] = bf16_lo(av4.x), av[1] = bf16_hi(av4.x), av[2] = bf16_lo(av4.y), av[3] = bf16_hi(av4.y);
+                            bv[0] = bf16_lo(bv4.x), bv[1] = bf16_hi(bv4.x), bv[2] = bf16_lo(bv4.y), bv[3] = bf16_hi(bv4.y);
+                        }
                         float da[4], db[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
@@ -1257,6 +1314,10 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                     bf16_t* orow = out + row * lout + sg * 2 * a.h + col;
                     store_groups(orow, wa_, ok);
                     store_groups(orow + a.h, wb_, ok);
+                    if constexpr (MODE == kModeDh8) {
+                        bf16_t* hid = reinterpret_cast<bf16_t*>(cur.shared ? a.hid_shared : a.hid_routed);
+                        store_groups(hid + row * lpre + sg * a.h + col, wh_, ok);
+                    }
                 }
             } else {
                 const int ldo = cur.shared ? a.S * a.h : a.h;
@@ -1282,6 +1343,40 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                         w[q][1] = pack_bf16x2(hv[2], hv[3]);
                     }
                     store_groups(out + row * ldo + cbase + pq * 32, w, ok);
+                    if constexpr (is_save8(MODE)) {
+                        // a and b in 8 bits, laid out as H: the 32 columns of
+                        // a row, held by lanes lr and lr + 32, are one block
+                        const int64_t at = row * ldo + cbase + pq * 32;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            float v[2][8];
+                            block_runs(acc[mb][2 * pq + t], v);
+                            uint32_t top = 0u;
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) top = max(top, abs_bits(v[p][u]));
+                            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
+                            const uint32_t scale = rows8_scale(top);
+                            const float inv = rows8_inverse(scale);
+                            uint8_t* codes = t == 0 ? (cur.shared ? a.pre_a_shared : a.pre_a_routed)
+                                                    : (cur.shared ? a.pre_b_shared : a.pre_b_routed);
+                            uint8_t* scales = t == 0 ? (cur.shared ? a.sc_a_shared : a.sc_a_routed)
+                                                     : (cur.shared ? a.sc_b_shared : a.sc_b_routed);
+                            if (ok) {
+#pragma unroll
+                                for (int p = 0; p < 2; ++p) {
+                                    const uint64_t lo = rows8_code4(v[p][0], v[p][1], v[p][2], v[p][3], inv);
+                                    const uint64_t hi = rows8_code4(v[p][4], v[p][5], v[p][6], v[p][7], inv);
+                                    *(__attribute__((address_space(1))) uint64_t*)(codes + at + 16 * p + 8 * lg) =
+                                        lo | (hi << 32);
+                                }
+                                if (lg == 0)
+                                    *(__attribute__((address_space(1))) uint8_t*)(scales + at / kRows8Block) =
+                                        static_cast<uint8_t>(scale);
+                            }
+                        }
+                    }
                     if constexpr (is_save(MODE)) {
                         // the pre-activations a, b (bf16), laid out as H
                         uint32_t wa_[4][2], wb_[4][2];
@@ -1547,18 +1642,49 @@ bool ffn_fused_plan(const moe_shape& s, int32_t* plan, FfnPlanArgs* fp) {
     return true;
 }
 
+// a and b in 8 bits: a_r, b_r [T*k, h] and a_s, b_s [T, S*h], each a rows8
+// buffer (h % 128 == 0: no padding)
+Saved8Layout saved8_layout(const moe_shape& s) {
+    Saved8Layout L;
+    const int64_t R = s.T * s.k, SH = static_cast<int64_t>(s.S) * s.h;
+    const size_t routed = rows8_bytes(R, s.h), shared = s.S > 0 ? rows8_bytes(s.T, SH) : 0;
+    L.a_r = 0;
+    L.b_r = routed;
+    L.a_s = 2 * routed;
+    L.b_s = L.a_s + shared;
+    L.bytes = L.b_s + shared;
+    L.scales_r = rows8_scales_at(R, s.h);
+    L.scales_s = s.S > 0 ? rows8_scales_at(s.T, SH) : 0;
+    return L;
+}
+
+namespace {
+void set_saved8(const moe_shape& s, GemmArgs& a, uint8_t* saved8) {
+    const Saved8Layout L = saved8_layout(s);
+    a.pre_a_routed = saved8 + L.a_r;
+    a.pre_b_routed = saved8 + L.b_r;
+    a.sc_a_routed = a.pre_a_routed + L.scales_r;
+    a.sc_b_routed = a.pre_b_routed + L.scales_r;
+    a.pre_a_shared = saved8 + L.a_s;
+    a.pre_b_shared = saved8 + L.b_s;
+    a.sc_a_shared = a.pre_a_shared + L.scales_s;
+    a.sc_b_shared = a.pre_b_shared + L.scales_s;
+}
+}  // namespace
+
 hipError_t launch_grouped_ffn(const moe_shape& s, const void* x_perm, const float* qparams,
                               const int32_t* offsets, const void* x, const void* w1,
                               const void* w3, const void* w2, void* y_perm, void* y_shared,
                               int32_t* plan, void* h_routed, void* h_shared, bool plan_done,
                               hipStream_t st, const Marks* mk, const int32_t* gather, void* pre_a_r,
-                              void* pre_b_r, void* pre_a_s, void* pre_b_s) {
+                              void* pre_b_r, void* pre_a_s, void* pre_b_s, void* saved8) {
     const bool f32 = s.act == MOE_F32;
     if (gather != nullptr && !ffn_gathers_rows(s)) return hipErrorInvalidValue;
     // with pre_a_r: the up-projection also stores a = W1 v and b = W3 v
     // (the persistent tiles only)
+    // with saved8: in 8 bits
     const bool save = pre_a_r != nullptr;
-    if (save && !use_big_tiles(s)) return hipErrorInvalidValue;
+    if ((save || saved8 != nullptr) && !use_big_tiles(s)) return hipErrorInvalidValue;
     const bool big = use_big_tiles(s);
     const int bm = f32 ? kF32BM : (big ? kBigBM : kBM);
     const PlanLayout pl = plan_layout(s);
@@ -1606,7 +1732,13 @@ hipError_t launch_grouped_ffn(const moe_shape& s, const void* x_perm, const floa
     a.pre_a_shared = static_cast<uint8_t*>(pre_a_s);
     a.pre_b_shared = static_cast<uint8_t*>(pre_b_s);
     hipError_t err;
-    if (save) {
+    if (saved8 != nullptr) {
+        set_saved8(s, a, static_cast<uint8_t*>(saved8));
+        a.ntn = 2 * s.h / kBigBN;
+        const int64_t mt = max_mtiles(s, bm, false);
+        err = s.dispatch == MOE_FP8_E4M3 ? launch_persistent<kModeUpFp8Save8>(a, mt, st)
+                                         : launch_persistent<kModeUpSave8>(a, mt, st);
+    } else if (save) {
         a.ntn = 2 * s.h / kBigBN;
         const int64_t mt = max_mtiles(s, bm, false);
         err = s.dispatch == MOE_FP8_E4M3 ? launch_persistent<kModeUpFp8Save>(a, mt, st)
@@ -1808,7 +1940,7 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
                                 const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh,
                                 int32_t* plan_f, int32_t* plan_dh, void* h_r, void* h_s, void* a_r,
                                 void* b_r, void* a_s, void* b_s, void* dd_r, void* dd_s,
-                                hipStream_t st, const Marks* mk, bool recompute) {
+                                hipStream_t st, const Marks* mk, bool recompute, const void* saved8) {
     const PlanLayout pf = plan_layout(s);
     const PlanLayout pd = plan_layout(s, (s.h + kBigBN - 1) / kBigBN, s.d / kBigBN);
     int32_t* cf = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(plan_f) + pf.counters);
@@ -1873,7 +2005,14 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
     a.out_routed = static_cast<uint8_t*>(dd_r);
     a.out_shared = static_cast<uint8_t*>(dd_s);
     a.ntn = pd.ntn_up;
-    err = launch_persistent<kModeDh>(a, max_mtiles(s, kBigBM, false), st);
+    if (saved8 != nullptr) {
+        set_saved8(s, a, static_cast<uint8_t*>(const_cast<void*>(saved8)));
+        a.hid_routed = static_cast<uint8_t*>(h_r);
+        a.hid_shared = static_cast<uint8_t*>(h_s);
+        err = launch_persistent<kModeDh8>(a, max_mtiles(s, kBigBM, false), st);
+    } else {
+        err = launch_persistent<kModeDh>(a, max_mtiles(s, kBigBM, false), st);
+    }
     mark(mk);
     if (err != hipSuccess) return err;
     // dx = [da | db] W13T^T: the down-projection with 2h hidden values

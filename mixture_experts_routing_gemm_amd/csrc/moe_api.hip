@@ -28,7 +28,8 @@ hipError_t launch_grouped_ffn(const moe_shape& s, const void* x_perm, const floa
                               int32_t* plan, void* h_routed, void* h_shared, bool plan_done,
                               hipStream_t st, const Marks* mk, const int32_t* gather = nullptr,
                               void* pre_a_r = nullptr, void* pre_b_r = nullptr, void* pre_a_s = nullptr,
-                              void* pre_b_s = nullptr);
+                              void* pre_b_s = nullptr, void* saved8 = nullptr);
+bool ffn_backward_big(const moe_shape& s);
 bool use_big_tiles(const moe_shape& s);
 // whether the whole-layer forward's up-projection reads its routed rows from
 // x through src_token (bf16 rows, persistent tiles) instead of from x_perm
@@ -63,9 +64,10 @@ hipError_t launch_grouped_ffn_f8w(const moe_shape& s, const void* x_perm, const 
 hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const float* qparams,
                                const int32_t* offsets, const void* x, const void* w1,
                                const void* w3, const void* w2, const void* dy_perm,
-                               const void* dy_sh, void* dx_perm, void* dx_sh, float* dw1,
-                               float* dw3, float* dw2, void* ws, hipStream_t st,
-                               const Marks* mk, const void* saved = nullptr);
+                               const void* dy_sh, void* dx_perm, void* dx_sh, void* dw1,
+                               void* dw3, void* dw2, void* ws, hipStream_t st,
+                               const Marks* mk, const void* saved = nullptr,
+                               const void* saved8 = nullptr, bool dw_bf16 = false);
 
 __global__ void clear_header_kernel(uint32_t* hdr) { hdr[threadIdx.x] = 0u; }
 
@@ -549,6 +551,71 @@ int32_t moe_grouped_ffn_backward_saved(const moe_shape* s, const void* x_perm,
                                           dy_shared, dx_perm, dx_shared, dw1, dw3, dw2,
                                           at<void>(ws, L.fbwd), static_cast<hipStream_t>(stream),
                                           nullptr, saved));
+}
+
+size_t moe_ffn_saved8_bytes(const moe_shape* s) {
+    if (check_shape(s, true) != MOE_OK || s->act != MOE_BF16 || !ffn_backward_big(*s)) return 0;
+    return saved8_layout(*s).bytes;
+}
+
+int32_t moe_grouped_ffn_save8(const moe_shape* s, const void* x_perm, const float* qparams,
+                              const int32_t* offsets, const void* x, const void* w1,
+                              const void* w3, const void* w2, void* y_perm, void* y_shared,
+                              void* saved8, size_t saved8_bytes, void* ws, size_t ws_bytes,
+                              void* stream) {
+    MOE_TRY(check_shape(s, true));
+    if (s->act != MOE_BF16 || !ffn_backward_big(*s)) return MOE_ERR_UNSUPPORTED;
+    if (s->T == 0) return MOE_OK;
+    MOE_TRY(check_ptrs({x_perm, offsets, w1, w3, w2, y_perm, saved8}));
+    if (s->S > 0) MOE_TRY(check_ptrs({x, y_shared}));
+    else if (y_shared != nullptr) return MOE_ERR_INVALID_ARG;
+    if (s->dispatch == MOE_FP8_E4M3) MOE_TRY(check_ptrs({qparams}));
+    MOE_TRY(check_opt({x, qparams}));
+    if (!aligned256(saved8) || saved8_bytes < saved8_layout(*s).bytes) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_ws(*s, MOE_STAGE_FFN, ws, ws_bytes));
+    const Layout L = layout(*s, MOE_STAGE_FFN);
+    return hip_status(launch_grouped_ffn(*s, x_perm, qparams, offsets, x, w1, w3, w2, y_perm,
+                                         y_shared, at<int32_t>(ws, L.plan), at<void>(ws, L.h_r),
+                                         at<void>(ws, L.h_s), false,
+                                         static_cast<hipStream_t>(stream), nullptr, nullptr, nullptr,
+                                         nullptr, nullptr, nullptr, saved8));
+}
+
+int32_t moe_grouped_ffn_backward_saved8(const moe_shape* s, const void* x_perm,
+                                        const float* qparams, const int32_t* offsets,
+                                        const void* x, const void* w1, const void* w3,
+                                        const void* w2, const void* saved8, size_t saved8_bytes,
+                                        const void* dy_perm, const void* dy_shared, void* dx_perm,
+                                        void* dx_shared, int32_t grad, void* dw1, void* dw3,
+                                        void* dw2, void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_shape(s, true));
+    if (s->act != MOE_BF16 || !ffn_backward_big(*s)) return MOE_ERR_UNSUPPORTED;
+    if (grad != MOE_F32 && grad != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    MOE_TRY(check_ptrs({w1, w3, w2, dw1, dw3, dw2}));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (s->T == 0) {
+        // no rows: every weight gradient is zero, in either type (d * h is a
+        // multiple of two)
+        const int64_t values = static_cast<int64_t>(s->E + s->S) * s->d * s->h;
+        const int64_t words = grad == MOE_F32 ? values : values / 2;
+        for (void* p : {dw1, dw3, dw2}) {
+            zero_f32_kernel<<<1024, 256, 0, st>>>(static_cast<float*>(p), words);
+            MOE_TRY(hip_status(hipGetLastError()));
+        }
+        return MOE_OK;
+    }
+    MOE_TRY(check_ptrs({saved8, x_perm, offsets, dy_perm, dx_perm}));
+    if (!aligned256(saved8) || saved8_bytes < saved8_layout(*s).bytes) return MOE_ERR_INVALID_ARG;
+    if (s->S > 0) MOE_TRY(check_ptrs({x, dy_shared, dx_shared}));
+    else if (dx_shared != nullptr || dy_shared != nullptr) return MOE_ERR_INVALID_ARG;
+    if (s->dispatch == MOE_FP8_E4M3) MOE_TRY(check_ptrs({qparams}));
+    MOE_TRY(check_opt({x, qparams}));
+    MOE_TRY(check_ws(*s, MOE_STAGE_FFN_BACKWARD, ws, ws_bytes));
+    const Layout L = layout(*s, MOE_STAGE_FFN_BACKWARD);
+    return hip_status(launch_ffn_backward(*s, x_perm, qparams, offsets, x, w1, w3, w2, dy_perm,
+                                          dy_shared, dx_perm, dx_shared, dw1, dw3, dw2,
+                                          at<void>(ws, L.fbwd), st, nullptr, nullptr, saved8,
+                                          grad == MOE_BF16));
 }
 
 size_t moe_fp8_weight_scale_floats(const moe_shape* s) {

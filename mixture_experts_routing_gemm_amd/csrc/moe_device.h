@@ -168,6 +168,12 @@ struct SavedLayout {
     size_t a_r = 0, b_r = 0, h_r = 0, a_s = 0, b_s = 0, h_s = 0, bytes = 0;
 };
 SavedLayout saved_layout(const moe_shape& s);
+// the same for a and b in 8 bits: byte offsets of the four rows8 buffers, and
+// of the scale bytes within a routed and within a shared one
+struct Saved8Layout {
+    size_t a_r = 0, b_r = 0, a_s = 0, b_s = 0, bytes = 0, scales_r = 0, scales_s = 0;
+};
+Saved8Layout saved8_layout(const moe_shape& s);
 
 struct GateMfmaPlan {
     bool use;
