@@ -22,6 +22,8 @@ namespace moe {
 constexpr int kMaxGroups = 256;
 
 enum LinearPass { kLinForward = 0, kLinDx = 1, kLinDw = 2 };
+// output tiles: 256 x 256, 256 x 128, 128 x 128, 64 x 128, 64 x 64
+enum LinTileShape { kLinTileBig = 0, kLinTileHalf = 1, kLinTileMid = 2, kLinTileSmall = 3, kLinTileTiny = 4 };
 
 struct LinearArgs {
     const uint8_t* a;        // x (forward), dz (dx, dW)
@@ -229,14 +231,14 @@ __device__ __forceinline__ void store8<float>(uint8_t* p, int64_t at, int nv, co
 // lanes (half = 0, 1): half h has columns c0 + 8 h .. +7 in v[0] and c0 + 16 +
 // 8 h .. +7 in v[1]. Adds the bias, keeps the pre-activation, applies fn, adds
 // the residual and stores. `ok`: the row exists (the same for both lanes; both
-// call this, whether it exists or not).
+// call this, whether it exists or not); cend: the first column not to store.
 template <typename T>
 __device__ __forceinline__ void linear_epilogue32(const LinearArgs& a, int g, int64_t row, int c0, int half,
-                                                  bool ok, float (&v)[2][8]) {
+                                                  bool ok, float (&v)[2][8], int cend) {
     int nv[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-        nv[p] = min(8, max(0, a.N - (c0 + 16 * p + 8 * half)));
+        nv[p] = min(8, max(0, cend - (c0 + 16 * p + 8 * half)));
         if (!ok) nv[p] = 0;
         if (a.bias != nullptr && nv[p] > 0) {
             float b[8];
@@ -322,22 +324,24 @@ __device__ __forceinline__ void block_runs(const f32x16& acc, float (&v)[2][8]) 
 
 // The store of one 32x32 block of C at rows m0 + lr, columns c0 ..: `row0` is
 // the first row of the group (forward, dx), `rows` the rows that exist.
-template <typename T, int PASS>
+// STAGED: of a kernel that stages its outputs, except for parts' sums and
+// float32 weight gradients.
+template <typename T, int PASS, bool STAGED>
 __device__ __forceinline__ void store_block(const LinearArgs& a, int g, int part, int64_t row0, int rows, int m,
                                             int c0, int half, const f32x16& acc) {
     float v[2][8];
     block_runs(acc, v);
     const bool ok = m < rows;
     const int64_t row = row0 + m;
-    if (a.part_out != nullptr) {
+    if ((STAGED && PASS != kLinDw) || a.part_out != nullptr) {
         const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
         plain_epilogue32<float>(reinterpret_cast<uint8_t*>(a.part_out), (part * all + row) * a.N, a.N, c0, half, ok, v);
     } else if constexpr (PASS == kLinForward) {
-        linear_epilogue32<T>(a, g, row, c0, half, ok, v);
+        linear_epilogue32<T>(a, g, row, c0, half, ok, v, a.N);
     } else if constexpr (PASS == kLinDx) {
         plain_epilogue32<T>(a.out, row * a.N, a.N, c0, half, ok, v);
     } else {
-        if (a.out_f32)
+        if (STAGED || a.out_f32)
             plain_epilogue32<float>(a.out, row * a.N, a.N, c0, half, ok, v);
         else
             plain_epilogue32<T>(a.out, row * a.N, a.N, c0, half, ok, v);
@@ -384,17 +388,18 @@ __device__ __forceinline__ void lin_supertile(int M, int N, int j, int& m, int& 
     m = 4 * mb + rr % hgt;
 }
 
-// k range of part s of `parts` of k values k_lo .. k_hi: whole slices of 32
+// k range of part s of `parts` of k values k_lo .. k_hi: whole slices of SK
+template <int SK>
 __device__ __forceinline__ void part_range(int k_lo, int k_hi, int s, int parts, int& k0, int& k1) {
     if (parts == 1) {
         k0 = k_lo;
         k1 = k_hi;
         return;
     }
-    const int slices = (k_hi - k_lo + 31) / 32;
+    const int slices = (k_hi - k_lo + SK - 1) / SK;
     const int per = (slices + parts - 1) / parts;
-    k0 = min(k_hi, k_lo + 32 * per * s);
-    k1 = min(k_hi, k0 + 32 * per);
+    k0 = min(k_hi, k_lo + SK * per * s);
+    k1 = min(k_hi, k0 + SK * per);
 }
 
 // The position `i` of this work-group's list -> tile, or false past its end.
@@ -403,9 +408,10 @@ __device__ __forceinline__ void part_range(int k_lo, int k_hi, int s, int parts,
 // round-robin to its work-groups: every m-tile takes equally long, and an
 // XCD's L2 sees few groups' weights. dW: tiles take as long as their group
 // has rows, so groups go longest first, and four tiles at a time to each XCD.
-template <int PASS, int BM, int BN>
+template <int PASS, int BM, int BN, int SK>
 __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w, const GroupOrder& o, int i,
                                          LinTile& t) {
+    t = LinTile{0, 0, 0, 0, 0, 0, 0, 0};
     const int xcd = blockIdx.x & 7, per_xcd = gridDim.x >> 3;
     const int c = static_cast<int>(blockIdx.x >> 3) + i * per_xcd;
     if constexpr (PASS == kLinDw) {
@@ -423,7 +429,7 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
         t.c0 = nt * BN;
         t.rows = a.M;
         t.row0 = static_cast<int64_t>(t.g) * a.M;
-        part_range(w.off[t.g], w.off[t.g + 1], t.part, a.parts, t.k0, t.k1);
+        part_range<SK>(w.off[t.g], w.off[t.g + 1], t.part, a.parts, t.k0, t.k1);
     } else {
         // (the launch bounds the list to 2^30 tiles)
         const int per_part = __builtin_amdgcn_readfirstlane(w.pre[a.G]) * a.ntn, total = per_part * a.parts;
@@ -439,7 +445,7 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
         t.c0 = nt * BN;
         t.rows = w.off[t.g + 1] - w.off[t.g];
         t.row0 = w.off[t.g];
-        part_range(0, a.K, t.part, a.parts, t.k0, t.k1);
+        part_range<SK>(0, a.K, t.part, a.parts, t.k0, t.k1);
     }
     // (the same for every lane by construction)
     t.g = __builtin_amdgcn_readfirstlane(t.g);
@@ -452,6 +458,163 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
     t.row0 = static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(t.row0)))) |
              (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(t.row0 >> 32))) << 32);
     return true;
+}
+
+// ------------------------------------------------------ staged epilogue --
+// A wave's WM x 64 block of a bf16 output, 32 rows at a time through 4 KB of
+// LDS (`stage`, this wave's own): lane (row, half) writes its runs of eight
+// columns as 16-byte chunks, at position chunk ^ (row / 2) % 8 of the row, and
+// reads back chunk lane % 8 of row lane / 8 + 8 i, so that a store writes 8
+// rows x 128 bytes. The wave's LDS accesses complete in order. `bias`: the
+// tile's bias in LDS (forward).
+__device__ __forceinline__ uint8_t* stage_at(uint8_t* stage, int row, int chunk) {
+    return stage + row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
+}
+// the staged 32 x 64 block at rows m .., columns c .. of a [.., N] bf16 array
+// whose row 0 is the group's first; the rows below `rows`, columns below N
+__device__ __forceinline__ void stage_out(const uint8_t* stage, uint8_t* out, int64_t row0, int rows, int N, int m, int c,
+                                          int lane) {
+    u32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load16(stage_at(const_cast<uint8_t*>(stage), 8 * i + (lane >> 3), lane & 7));
+    const int col = c + 8 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = m + 8 * i + (lane >> 3);
+        if (r < rows && col < N)
+            *(__attribute__((address_space(1))) u32x4*)(out + ((row0 + r) * N + col) * 2) = v[i];
+    }
+}
+
+template <int PASS, int MB, int NB>
+__device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const LinTile& t, int mw, int cw, uint8_t* stage,
+                                                  const float* bias, int lane, f32x16 (&acc)[MB][NB]) {
+    static_assert(NB == 2, "64 columns a wave");
+    // (the addresses below depend on the lane alone: computed before the tile
+    // loop and kept, they took more registers than there are)
+    asm volatile("" : "+v"(lane));
+    const int lr = lane & 31, half = lane >> 5;
+    if constexpr (PASS != kLinForward) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float v[2][8];
+                block_runs(acc[mb][nb], v);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
+            }
+            stage_out(stage, a.out, t.row0, t.rows, a.N, mw + 32 * mb, cw, lane);
+        }
+    } else {
+        // this lane's columns: cw + 32 nb + 16 p + 8 half .. +7; z of one block
+        const auto in = [&](int nb, int p) { return cw + 32 * nb + 16 * p + 8 * half < a.N; };
+        auto z_runs = [&](int mb, int nb, float (&v)[2][8]) {
+            // (computed anew for each use: kept from one to the next, z of a
+            // whole block row cost 32 registers, and the compiler spilled)
+            asm volatile("" : "+v"(acc[mb][nb]));
+            block_runs(acc[mb][nb], v);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(bias + cw - t.c0 + 32 * nb + 16 * p + 8 * half + 4 * q);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v[p][4 * q + u] += b[u];
+                }
+        };
+        // the residual of the next 32 rows is loaded before this one's stores:
+        // a load after them would complete after them
+        u32x4 res[2][NB][2];
+        auto load_residual = [&](int mb, u32x4 (&r)[NB][2]) {
+            const int m = mw + 32 * mb + lr;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    r[nb][p] = u32x4{0u, 0u, 0u, 0u};
+                    if (m < t.rows && in(nb, p))
+                        r[nb][p] = *(const __attribute__((address_space(1))) u32x4*)(
+                            a.residual + ((t.row0 + m) * a.N + cw + 32 * nb + 16 * p + 8 * half) * 2);
+                }
+        };
+        if (a.residual != nullptr) load_residual(0, res[0]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            if (a.residual != nullptr && mb + 1 < MB) load_residual(mb + 1, res[(mb + 1) & 1]);
+            const int m = mw + 32 * mb;
+            if (a.zsave != nullptr) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float v[2][8];
+                    z_runs(mb, nb, v);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
+                }
+                stage_out(stage, a.zsave, t.row0, t.rows, a.N, m, cw, lane);
+            }
+            if (a.codes != nullptr) {
+                // 64 codes a row, 16 bytes at position chunk ^ (row / 2) % 4
+                const int64_t nblk = a.n32 / kRows8Block;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float v[2][8];
+                    z_runs(mb, nb, v);
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            v[p][u] = in(nb, p) ? v[p][u] : 0.0f;  // (the padding's codes are 0)
+                            top = max(top, abs_bits(v[p][u]));
+                        }
+                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
+                    const uint32_t scale = rows8_scale(top);
+                    const float inv = rows8_inverse(scale);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        uint2 w;
+                        w.x = rows8_code4(v[p][0], v[p][1], v[p][2], v[p][3], inv);
+                        w.y = rows8_code4(v[p][4], v[p][5], v[p][6], v[p][7], inv);
+                        *reinterpret_cast<uint2*>(stage + lr * 64 + (((2 * nb + p) ^ ((lr >> 1) & 3)) << 4) + 8 * half) = w;
+                    }
+                    if (half == 0 && m + lr < t.rows && cw + 32 * nb < a.N)
+                        *(__attribute__((address_space(1))) uint8_t*)(
+                            a.scales + (t.row0 + m + lr) * nblk + (cw + 32 * nb) / kRows8Block) =
+                            static_cast<uint8_t>(scale);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * i + (lane >> 2), c = lane & 3;
+                    const u32x4 w = load16(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                    if (m + r < t.rows && cw + 16 * c < a.n32)
+                        *(__attribute__((address_space(1))) u32x4*)(a.codes + (t.row0 + m + r) * a.n32 + cw + 16 * c) = w;
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float v[2][8];
+                z_runs(mb, nb, v);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (a.fn != MOE_FN_NONE) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[p][u] = lin_fn(a.fn, v[p][u]);
+                    }
+                    if (a.residual != nullptr) {
+                        float r[8];
+                        ActVec<bf16_t>::unpack(res[mb & 1][nb][p], r);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[p][u] += r[u];
+                    }
+                    store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
+                }
+            }
+            stage_out(stage, a.out, t.row0, t.rows, a.N, m, cw, lane);
+        }
+    }
 }
 
 }  // namespace moe

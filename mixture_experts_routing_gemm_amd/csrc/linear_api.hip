@@ -22,8 +22,8 @@ struct DzArgs {
 };
 
 int device_cus();
-hipError_t launch_linear_bf16(int pass, const LinearArgs& a, int shape, hipStream_t st);
-hipError_t launch_linear_f32(int pass, const LinearArgs& a, int shape, hipStream_t st);
+hipError_t launch_linear_tile(int pass, const LinearArgs& a, int shape, bool f32, hipStream_t st);
+hipError_t launch_linear_rows(const LinearArgs& a, int fb, hipStream_t st);
 hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st);
 int64_t linear_db_tiles(int64_t R, int G);
 hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st);
@@ -64,17 +64,67 @@ size_t saved_size(const moe_linear_shape& s) {
 struct Plan {
     int shape, parts;
 };
+
+// The microseconds that a compute unit takes for one slice of k (64 bytes) of
+// one tile: `full` with every unit at work on as many tiles as it holds, `one`
+// for a tile that has a unit to itself in a round that is not full. Measured
+// at 4096 values of k on an MI355X (forward, dx and dW alike):
+// bf16 256 x 256 tiles reach 1.13 PFLOP/s, 256 x 128 0.94, 128 x 128 0.82 and
+// 64 x 128 0.63, float32 128 x 128 132 TFLOP/s and 64 x 64 121; smaller tiles
+// win where the larger ones leave units idle.
+struct TileCost {
+    int shape, bm, bn;
+    float full, one;
+};
+constexpr TileCost kBf16Tiles[] = {{kLinTileBig, 256, 256, 0.94f, 0.64f},
+                                   {kLinTileHalf, 256, 128, 0.57f, 0.52f},
+                                   {kLinTileMid, 128, 128, 0.33f, 0.33f},
+                                   {kLinTileSmall, 64, 128, 0.215f, 0.24f}};
+constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f}, {kLinTileTiny, 64, 64, 0.276f, 0.4f}};
+
+// The cheapest tile shape and number of parts by those costs: whole rounds of
+// the units, the last one in between, and for parts the join: about 7 us, and
+// its float32 sums written and read at 4 TB/s. The rows of a group are not
+// known here: half a tile of each group is taken to be empty.
 Plan plan_of(const moe_linear_shape& s, int pass) {
-    Plan p{0, 1};
-    const int64_t avg = s.rows / s.groups;
-    if (s.act == MOE_F32) {
-        p.shape = pass == kLinDw ? (s.n_out >= 128 && s.n_in >= 128 ? 0 : 1) : (avg >= 96 ? 0 : 1);
-    } else if (pass == kLinDw) {
-        p.shape = s.n_out >= 256 && s.n_in >= 256 ? 0 : 1;
-    } else {
-        p.shape = avg >= 192 ? 0 : (avg >= 96 ? 1 : 2);
+    const bool f32 = s.act == MOE_F32;
+    const TileCost* const first = f32 ? kF32Tiles : kBf16Tiles;
+    const TileCost* const last = first + (f32 ? 2 : pass == kLinDw ? 3 : 4);
+    const int64_t units = device_cus(), sk = f32 ? 16 : 32;
+    const int64_t n = pass == kLinForward ? s.n_out : s.n_in, groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
+    const int64_t k = pass == kLinForward ? s.n_in : pass == kLinDx ? s.n_out : s.rows / groups;
+    const int64_t slices = std::max<int64_t>(1, (k + sk - 1) / sk);
+    const double values = static_cast<double>(pass == kLinDw ? static_cast<int64_t>(s.groups) * s.n_out : s.rows) * n;
+    Plan best{first->shape, 1};
+    double least = -1.0;
+    for (const TileCost* c = first; c != last; ++c) {
+        const int64_t mt = pass == kLinDw ? groups * ((s.n_out + c->bm - 1) / c->bm)
+                                          : s.groups == 1 ? (s.rows + c->bm - 1) / c->bm : s.rows / c->bm + (groups + 1) / 2;
+        const int64_t tiles = mt * ((n + c->bn - 1) / c->bn);
+        for (int parts = 1; parts <= 16 && parts * 4 <= slices + 3; ++parts) {
+            if (parts > 1 && tiles * parts > 4 * units) break;
+            const int64_t each = (slices + parts - 1) / parts, all = tiles * parts;
+            const double rest = static_cast<double>(all % units) / units;
+            const double round = all / units * c->full + (rest > 0.0 ? c->one + (c->full - c->one) * rest : 0.0);
+            double us = each * round;
+            if (parts > 1) us += 7.0 + values * 8.0 * parts / 4e6;
+            if (least < 0.0 || us < least) {
+                least = us;
+                best = Plan{c->shape, parts};
+            }
+        }
     }
-    return p;
+    return best;
+}
+
+// The forward by the kernel for few rows: where the 64 x 128 tiles of all
+// groups would leave units idle, that kernel's narrower columns keep them
+// reading (one row, 4096 -> 4096: 9 us, the tiles in four parts 20; 8 groups of
+// 4 rows, 2048 -> 1408: 16 against 19, of 16 rows 20 against 19).
+bool few_rows(const moe_linear_shape& s) {
+    const int64_t groups = std::min<int64_t>(s.groups, s.rows);
+    return s.act == MOE_BF16 && s.rows <= s.groups * int64_t(s.groups == 1 ? 32 : 8) &&
+           groups * ((s.n_out + 127) / 128) < device_cus();
 }
 
 struct LinLayout {
@@ -116,11 +166,18 @@ int32_t check_saved(const moe_linear_shape& s, const void* saved, size_t saved_b
 }
 
 hipError_t run_product(const moe_linear_shape& s, int pass, LinearArgs a, void* ws, size_t part_at, hipStream_t st) {
+    if (pass == kLinForward && few_rows(s)) {
+        a.parts = 1;
+        // 16 columns a work-group where 32 would leave compute units idle
+        // (8-bit codes need 32: a block)
+        const int64_t blocks = static_cast<int64_t>(s.groups) * ((s.n_out + 31) / 32);
+        return launch_linear_rows(a, s.save != MOE_SAVE_INT8 && blocks < device_cus() ? 1 : 2, st);
+    }
     const Plan p = plan_of(s, pass);
     const bool f32 = s.act == MOE_F32;
     a.parts = p.parts;
     a.part_out = p.parts > 1 ? at<float>(ws, part_at) : nullptr;
-    const hipError_t e = f32 ? launch_linear_f32(pass, a, p.shape, st) : launch_linear_bf16(pass, a, p.shape, st);
+    const hipError_t e = launch_linear_tile(pass, a, p.shape, f32, st);
     if (e != hipSuccess || p.parts == 1) return e;
     return launch_linear_join(pass, a, f32, st);
 }

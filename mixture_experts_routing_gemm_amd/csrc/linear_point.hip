@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
         }
     }
     if constexpr (PASS == kLinForward) {
-        linear_epilogue32<T>(a, g, row, c0, half, ok, v);
+        linear_epilogue32<T>(a, g, row, c0, half, ok, v, a.N);
     } else if (PASS == kLinDw && a.out_f32) {
         plain_epilogue32<float>(a.out, row * a.N, a.N, c0, half, ok, v);
     } else {
