@@ -418,18 +418,43 @@ _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 
 
 def _t(t, dtype, numel, name):
-    """The pointer of a tensor that must be there, of this type and size, on the current GPU."""
+    """The address of a tensor that must be there, of this type and size, on the current GPU."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype or t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} values of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    return _addr(t, name)
+
+
+def _addr(t, name):
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the MoE library must be on the GPU")
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return _p(t)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the MoE library must be contiguous")
+    return t.data_ptr()
 
 
 def _t0(t, dtype, numel, name):
     return None if t is None else _t(t, dtype, numel, name)
+
+
+def _buf(b, name):
+    """(address, bytes) of a caller buffer, (None, 0) without one."""
+    return (None, 0) if b is None else (_addr(b, name), b.numel() * b.element_size())
+
+
+# (the current device's index and its current stream without the objects that
+# torch.cuda makes of them: a call of a small layer is as long as its launch)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _stream(stream):
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(_current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def moe_linear_workspace_bytes(shape: moe_linear_shape, stage: int) -> int:
@@ -465,35 +490,35 @@ def _linear_operands(s):
 
 def moe_grouped_linear(shape, x, offsets, w, bias, residual, y, saved, ws, stream=None):
     act, nx, ny, nw = _linear_operands(shape)
-    sv, sn = _ws(saved)
-    wp, wn = _ws(ws)
+    sv, sn = _buf(saved, "saved")
+    wp, wn = _buf(ws, "ws")
     _check(lib.moe_grouped_linear(
         ctypes.byref(shape), _t(x, act, nx, "x"), _t(offsets, torch.int32, shape.groups + 1, "offsets"),
         _t(w, act, nw, "w"), _t0(bias, torch.float32, shape.groups * shape.n_out, "bias"),
-        _t0(residual, act, ny, "residual"), _t(y, act, ny, "y"), sv, sn, wp, wn, _s(stream)),
+        _t0(residual, act, ny, "residual"), _t(y, act, ny, "y"), sv, sn, wp, wn, _stream(stream)),
         "moe_grouped_linear")
 
 
 def moe_linear(shape, x, w, bias, residual, y, saved, ws, stream=None):
     act, nx, ny, nw = _linear_operands(shape)
-    sv, sn = _ws(saved)
-    wp, wn = _ws(ws)
+    sv, sn = _buf(saved, "saved")
+    wp, wn = _buf(ws, "ws")
     _check(lib.moe_linear(
         ctypes.byref(shape), _t(x, act, nx, "x"), _t(w, act, nw, "w"),
         _t0(bias, torch.float32, shape.groups * shape.n_out, "bias"), _t0(residual, act, ny, "residual"),
-        _t(y, act, ny, "y"), sv, sn, wp, wn, _s(stream)), "moe_linear")
+        _t(y, act, ny, "y"), sv, sn, wp, wn, _stream(stream)), "moe_linear")
 
 
 def _linear_backward(name, shape, x, offsets, w, saved, dy, dx, dw, db, ws, stream):
     act, nx, ny, nw = _linear_operands(shape)
     grad = _TORCH.get(shape.grad)
-    sv, sn = _ws(saved)
-    wp, wn = _ws(ws)
+    sv, sn = _buf(saved, "saved")
+    wp, wn = _buf(ws, "ws")
     off = () if offsets is None else (_t(offsets, torch.int32, shape.groups + 1, "offsets"),)
     _check(getattr(lib, name)(
         ctypes.byref(shape), _t0(x, act, nx, "x"), *off, _t0(w, act, nw, "w"), sv, sn,
         _t0(dy, act, ny, "dy"), _t0(dx, act, nx, "dx"), _t0(dw, grad, nw, "dw"),
-        _t0(db, grad, shape.groups * shape.n_out, "db"), wp, wn, _s(stream)), name)
+        _t0(db, grad, shape.groups * shape.n_out, "db"), wp, wn, _stream(stream)), name)
 
 
 def moe_grouped_linear_backward(shape, x, offsets, w, saved, dy, dx, dw, db, ws, stream=None):
@@ -530,14 +555,14 @@ def _rows8(x):
 
 def moe_pack_rows8(x, packed, stream=None):
     rows, n, code = _rows8(x)
-    pp, pn = _ws(packed)
-    _check(lib.moe_pack_rows8(rows, n, code, _p(x), pp, pn, _s(stream)), "moe_pack_rows8")
+    pp, pn = _buf(packed, "packed")
+    _check(lib.moe_pack_rows8(rows, n, code, _addr(x, "x"), pp, pn, _stream(stream)), "moe_pack_rows8")
 
 
 def moe_unpack_rows8(packed, x, stream=None):
     rows, n, code = _rows8(x)
-    pp, pn = _ws(packed)
-    _check(lib.moe_unpack_rows8(rows, n, code, pp, pn, _p(x), _s(stream)), "moe_unpack_rows8")
+    pp, pn = _buf(packed, "packed")
+    _check(lib.moe_unpack_rows8(rows, n, code, pp, pn, _addr(x, "x"), _stream(stream)), "moe_unpack_rows8")
 
 
 def moe_ffn_saved8_bytes(shape) -> int:
@@ -554,18 +579,18 @@ def alloc_saved8(shape, device="cuda"):
 
 def moe_grouped_ffn_save8(shape, x_perm, qparams, offsets, x, w1, w3, w2, y_perm, y_shared, saved8, ws,
                           stream=None):
-    wp, wn = _ws(ws)
-    sv, sn = _ws(saved8)
+    wp, wn = _buf(ws, "ws")
+    sv, sn = _buf(saved8, "saved8")
     _check(lib.moe_grouped_ffn_save8(ctypes.byref(shape), _p(x_perm), _p(qparams), _p(offsets), _p(x),
                                      _p(w1), _p(w3), _p(w2), _p(y_perm), _p(y_shared), sv, sn, wp, wn,
-                                     _s(stream)), "moe_grouped_ffn_save8")
+                                     _stream(stream)), "moe_grouped_ffn_save8")
 
 
 def moe_grouped_ffn_backward_saved8(shape, x_perm, qparams, offsets, x, w1, w3, w2, saved8, dy_perm,
                                     dy_shared, dx_perm, dx_shared, grad, dw1, dw3, dw2, ws, stream=None):
     """grad: the type of dw1, dw3 and dw2, "f32" or "bf16"."""
-    wp, wn = _ws(ws)
-    sv, sn = _ws(saved8)
+    wp, wn = _buf(ws, "ws")
+    sv, sn = _buf(saved8, "saved8")
     g = _DTYPES[grad] if isinstance(grad, str) else int(grad)
     n = (shape.E + shape.S) * shape.d * shape.h
     if g not in _TORCH:
@@ -573,5 +598,5 @@ def moe_grouped_ffn_backward_saved8(shape, x_perm, qparams, offsets, x, w1, w3, 
     _check(lib.moe_grouped_ffn_backward_saved8(
         ctypes.byref(shape), _p(x_perm), _p(qparams), _p(offsets), _p(x), _p(w1), _p(w3), _p(w2), sv, sn,
         _p(dy_perm), _p(dy_shared), _p(dx_perm), _p(dx_shared), g, _t(dw1, _TORCH[g], n, "dw1"),
-        _t(dw3, _TORCH[g], n, "dw3"), _t(dw2, _TORCH[g], n, "dw2"), wp, wn, _s(stream)),
+        _t(dw3, _TORCH[g], n, "dw3"), _t(dw2, _TORCH[g], n, "dw2"), wp, wn, _stream(stream)),
         "moe_grouped_ffn_backward_saved8")

@@ -51,49 +51,54 @@ struct LinearArgs {
 };
 
 // ------------------------------------------------------------ functions --
-__device__ __forceinline__ float lin_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
-
-// Phi(v), the normal distribution's integral, from Abramowitz and Stegun's
-// formula 7.1.26 for erf (off by at most 1.5e-7): with x = |v| / sqrt(2) and
-// t = 1 / (1 + 0.3275911 x), erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5))))
-// e^(-x x). Also gives e = e^(-v v / 2), which the slope needs too.
-__device__ __forceinline__ float normal_cdf(float v, float& e) {
-    const float x = __builtin_fabsf(v) * 0.70710678118654752f;
-    e = __expf(-x * x);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-    float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
-    p = __builtin_fmaf(p, t, 1.421413741f);
-    p = __builtin_fmaf(p, t, -0.284496736f);
-    p = __builtin_fmaf(p, t, 0.254829592f);
-    const float half_tail = 0.5f * p * t * e;  // Phi(-|v|)
-    return v < 0.0f ? half_tail : 1.0f - half_tail;
+// (A 256 x 256 tile's epilogue is bound by its vector instructions, 4 cycles
+// each and 16 for exp and rcp: 128 values a lane, two waves a SIMD. The forms
+// below are the ones with the fewest.)
+__device__ __forceinline__ float lin_sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
 }
 
-// (the comparisons are written so that a NaN stays one, and gelu(-inf),
-// silu(-inf) are 0: the product of -inf with a zero would be a NaN)
+// Phi(-|v|), the normal distribution's tail, from Abramowitz and Stegun's
+// formula 7.1.26 for erf (off by at most 1.5e-7): with x = |v| / sqrt(2) and
+// t = 1 / (1 + 0.3275911 x), erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5))))
+// e^(-x x), and Phi(-|v|) = erfc(x) / 2 (the halves are in the coefficients).
+// Also gives e = e^(-v v / 2) = 2^(-s s), s = v sqrt(log2(e) / 2).
+__device__ __forceinline__ float normal_tail(float v, float& e) {
+    const float s = v * 0.849321800288019f;
+    e = __builtin_amdgcn_exp2f(-(s * s));
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.27273748f, __builtin_fabsf(s), 1.0f));
+    float p = __builtin_fmaf(0.5307027145f, t, -0.7265760135f);
+    p = __builtin_fmaf(p, t, 0.7107068705f);
+    p = __builtin_fmaf(p, t, -0.142248368f);
+    p = __builtin_fmaf(p, t, 0.127414796f);
+    return p * t * e;
+}
+
+// (the bounds on z keep an infinity from meeting a zero factor: gelu(-inf) and
+// silu(-inf) are 0, gelu(inf) is inf; a NaN stays one through the other factor)
 __device__ __forceinline__ float lin_fn(int fn, float z) {
     if (fn == MOE_FN_RELU) return z < 0.0f ? 0.0f : z;
     if (fn == MOE_FN_GELU) {
+        // z >= 0: z (1 - tail); z < 0: z tail
         float e;
-        const float c = normal_cdf(z, e);
-        return c == 0.0f ? 0.0f : z * c;
+        const float tail = normal_tail(z, e);
+        return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), 64.0f), tail, __builtin_fmaxf(z, 0.0f));
     }
-    if (fn == MOE_FN_SILU) {
-        const float s = lin_sigmoid(z);
-        return s == 0.0f ? 0.0f : z * s;
-    }
+    if (fn == MOE_FN_SILU) return __builtin_fmaxf(z, -1e4f) * lin_sigmoid(z);
     return z;
 }
 __device__ __forceinline__ float lin_slope(int fn, float z) {
     if (fn == MOE_FN_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     if (fn == MOE_FN_GELU) {
+        // Phi(z) + z times the density, e / sqrt(2 pi)
         float e;
-        const float c = normal_cdf(z, e);
-        return e == 0.0f ? c : __builtin_fmaf(z * e, 0.39894228040143268f, c);
+        const float tail = normal_tail(z, e);
+        const float cdf = 0.5f + __builtin_copysignf(0.5f - tail, z);
+        return __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -64.0f, 64.0f) * e, 0.39894228040143268f, cdf);
     }
     if (fn == MOE_FN_SILU) {
         const float s = lin_sigmoid(z);
-        return s == 0.0f ? 0.0f : (s == 1.0f ? 1.0f : s * __builtin_fmaf(z, 1.0f - s, 1.0f));
+        return s * __builtin_fmaf(__builtin_amdgcn_fmed3f(z, -1e4f, 1e4f), 1.0f - s, 1.0f);
     }
     return 1.0f;
 }
@@ -108,7 +113,8 @@ struct GroupWalk {
     int pre[kMaxGroups + 1];
 };
 
-// by every thread of a work-group of at least one wave; ends with a barrier
+// by every thread of a work-group of at least one wave; ends with a barrier.
+// hdr: the workspace's header (one work-group of a launch reports), or NULL
 __device__ __forceinline__ void walk_groups(GroupWalk& w, const int32_t* __restrict__ offsets, int64_t R, int G,
                                             int bm, uint32_t* hdr) {
     const int R32 = static_cast<int>(R);
@@ -155,7 +161,7 @@ __device__ __forceinline__ void walk_groups(GroupWalk& w, const int32_t* __restr
                     w.off[g] = v[i];
                 }
             }
-            if (bad && blockIdx.x == 0 && blockIdx.y == 0) set_error(hdr, 1u);
+            if (bad) set_error(hdr, 1u);
             // (one wave: its LDS accesses complete in order)
             __builtin_amdgcn_wave_barrier();
             int sum = 0, t[5];
@@ -402,18 +408,18 @@ __device__ __forceinline__ void part_range(int k_lo, int k_hi, int s, int parts,
     k1 = min(k_hi, k0 + SK * per);
 }
 
-// The position `i` of this work-group's list -> tile, or false past its end.
-// Forward and dx: the list of tiles (part by part, group by group) is cut into
+// The position `i` of the list of work-group `bid` of `nblk` (a multiple of 8,
+// bid % 8 the XCD) -> tile, or false past its end. Forward and dx: the list of tiles (part by part, group by group) is cut into
 // eight equal runs, one for each XCD (work-groups b with b % 8 = x), dealt
 // round-robin to its work-groups: every m-tile takes equally long, and an
 // XCD's L2 sees few groups' weights. dW: tiles take as long as their group
 // has rows, so groups go longest first, and four tiles at a time to each XCD.
 template <int PASS, int BM, int BN, int SK>
-__device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w, const GroupOrder& o, int i,
-                                         LinTile& t) {
+__device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w, const GroupOrder& o, int bid, int nblk,
+                                         int i, LinTile& t) {
     t = LinTile{0, 0, 0, 0, 0, 0, 0, 0};
-    const int xcd = blockIdx.x & 7, per_xcd = gridDim.x >> 3;
-    const int c = static_cast<int>(blockIdx.x >> 3) + i * per_xcd;
+    const int xcd = bid & 7, per_xcd = nblk >> 3;
+    const int c = (bid >> 3) + i * per_xcd;
     if constexpr (PASS == kLinDw) {
         const int per_group = a.mtiles * a.ntn;
         const int total = a.G * per_group * a.parts;
@@ -557,6 +563,8 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
             }
             if (a.codes != nullptr) {
                 // 64 codes a row, 16 bytes at position chunk ^ (row / 2) % 4
+                // (past N the weights and the bias read as zeros, and so z:
+                // the padding's codes are 0)
                 const int64_t nblk = a.n32 / kRows8Block;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
@@ -566,10 +574,7 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            v[p][u] = in(nb, p) ? v[p][u] : 0.0f;  // (the padding's codes are 0)
-                            top = max(top, abs_bits(v[p][u]));
-                        }
+                        for (int u = 0; u < 8; ++u) top = max(top, abs_bits(v[p][u]));
                     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
                     const uint32_t scale = rows8_scale(top);
                     const float inv = rows8_inverse(scale);
@@ -614,6 +619,60 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
             }
             stage_out(stage, a.out, t.row0, t.rows, a.N, m, cw, lane);
         }
+    }
+}
+
+// ------------------------------------------------------- bias gradient --
+// rows that one work-group of the dz kernel sums into one partial. (32768 x
+// 1408: 64 us at 32 rows, 72 at 64, 86 at 128, where every work-group starts
+// at once and they load and compute in step; 512 x 128: 8 against 15.)
+constexpr int kDzRows = 32;
+
+struct DbArgs {
+    const int32_t* offsets;
+    int64_t R;
+    int G, N;
+    const float* part;   // [blocks of kDzRows rows of a group][N], or NULL:
+    const uint8_t* dy;   //   the sums are taken of dy [R, N] (act) itself
+    void* db;            // [G, N]
+    int db_f32;
+};
+
+// db of group g, columns 64 cb .. +63: SPLIT threads a column, each every
+// SPLIT-th partial (or row) in order, then their sums in order. No atomics:
+// the same bits every call. By 64 SPLIT threads.
+template <typename T, int SPLIT>
+__device__ __forceinline__ void linear_db_block(const DbArgs& a, int g, int cb) {
+    __shared__ GroupWalk walk;
+    __shared__ float sums[SPLIT][64];
+    walk_groups(walk, a.offsets, a.R, a.G, kDzRows, nullptr);
+    const int c = threadIdx.x & 63, col = cb * 64 + c, q = threadIdx.x >> 6;
+    float s = 0.0f;
+    if (col < a.N) {
+        if (a.part != nullptr) {
+            const int end = walk.pre[g + 1];
+#pragma unroll 8
+            for (int t = walk.pre[g] + q; t < end; t += SPLIT) s += a.part[static_cast<int64_t>(t) * a.N + col];
+        } else {
+            const int end = walk.off[g + 1];
+            const T* dy = reinterpret_cast<const T*>(a.dy);
+#pragma unroll 8
+            for (int r = walk.off[g] + q; r < end; r += SPLIT) {
+                const T v = dy[static_cast<int64_t>(r) * a.N + col];
+                if constexpr (sizeof(T) == 4) s += v;
+                else s += bf16_to_f32(v);
+            }
+        }
+    }
+    sums[q][c] = s;
+    __syncthreads();
+    if (q == 0 && col < a.N) {
+        float t = sums[0][c];
+#pragma unroll
+        for (int i = 1; i < SPLIT; ++i) t += sums[i][c];
+        const int64_t at = static_cast<int64_t>(g) * a.N + col;
+        if (a.db_f32) static_cast<float*>(a.db)[at] = t;
+        else static_cast<bf16_t*>(a.db)[at] = f32_to_bf16(t);
     }
 }
 

@@ -27,8 +27,8 @@ hipError_t launch_linear_rows(const LinearArgs& a, int fb, hipStream_t st);
 hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st);
 int64_t linear_db_tiles(int64_t R, int G);
 hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st);
-hipError_t launch_linear_db(const int32_t* offsets, int64_t R, int G, int N, const float* part, void* db, bool f32,
-                            hipStream_t st);
+hipError_t launch_linear_db(const DbArgs& a, bool f32, hipStream_t st);
+hipError_t launch_linear_backward(const LinearArgs& x, const LinearArgs& w, const DbArgs& d, bool f32, hipStream_t st);
 hipError_t launch_pack_rows8(int64_t rows, int n, bool f32, const void* x, void* packed, hipStream_t st);
 hipError_t launch_unpack_rows8(int64_t rows, int n, bool f32, const void* packed, void* x, hipStream_t st);
 
@@ -63,6 +63,7 @@ size_t saved_size(const moe_linear_shape& s) {
 // How a product is run: its tile shape and in how many parts k is split.
 struct Plan {
     int shape, parts;
+    float us;  // its estimate
 };
 
 // The microseconds that a compute unit takes for one slice of k (64 bytes) of
@@ -72,15 +73,17 @@ struct Plan {
 // bf16 256 x 256 tiles reach 1.13 PFLOP/s, 256 x 128 0.94, 128 x 128 0.82 and
 // 64 x 128 0.63, float32 128 x 128 132 TFLOP/s and 64 x 64 121; smaller tiles
 // win where the larger ones leave units idle.
+// `epilogue`: what an activation and saved pre-activations each add to a tile (two work-groups on a unit hide half of it in each other's
+// products).
 struct TileCost {
     int shape, bm, bn;
-    float full, one;
+    float full, one, epilogue;
 };
-constexpr TileCost kBf16Tiles[] = {{kLinTileBig, 256, 256, 0.94f, 0.64f},
-                                   {kLinTileHalf, 256, 128, 0.57f, 0.52f},
-                                   {kLinTileMid, 128, 128, 0.33f, 0.33f},
-                                   {kLinTileSmall, 64, 128, 0.215f, 0.24f}};
-constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f}, {kLinTileTiny, 64, 64, 0.276f, 0.4f}};
+constexpr TileCost kBf16Tiles[] = {{kLinTileBig, 256, 256, 0.96f, 0.64f, 8.0f},
+                                   {kLinTileHalf, 256, 128, 0.57f, 0.52f, 3.0f},
+                                   {kLinTileMid, 128, 128, 0.345f, 0.33f, 1.5f},
+                                   {kLinTileSmall, 64, 128, 0.215f, 0.24f, 0.8f}};
+constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f, 1.0f}, {kLinTileTiny, 64, 64, 0.276f, 0.4f, 0.5f}};
 
 // The cheapest tile shape and number of parts by those costs: whole rounds of
 // the units, the last one in between, and for parts the join: about 7 us, and
@@ -91,27 +94,27 @@ Plan plan_of(const moe_linear_shape& s, int pass) {
     const TileCost* const first = f32 ? kF32Tiles : kBf16Tiles;
     const TileCost* const last = first + (f32 ? 2 : pass == kLinDw ? 3 : 4);
     const int64_t units = device_cus(), sk = f32 ? 16 : 32;
-    const int64_t n = pass == kLinForward ? s.n_out : s.n_in, groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
+    const int64_t n = pass == kLinForward ? s.n_out : s.n_in;
+    const int64_t groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
     const int64_t k = pass == kLinForward ? s.n_in : pass == kLinDx ? s.n_out : s.rows / groups;
     const int64_t slices = std::max<int64_t>(1, (k + sk - 1) / sk);
-    const double values = static_cast<double>(pass == kLinDw ? static_cast<int64_t>(s.groups) * s.n_out : s.rows) * n;
-    Plan best{first->shape, 1};
-    double least = -1.0;
+    const float values = static_cast<float>(pass == kLinDw ? static_cast<int64_t>(s.groups) * s.n_out : s.rows) * n;
+    const float extras = pass != kLinForward ? 0.0f
+                                             : static_cast<float>((s.fn != MOE_FN_NONE) + (s.save != MOE_SAVE_NONE));
+    Plan best{first->shape, 1, -1.0f};
     for (const TileCost* c = first; c != last; ++c) {
         const int64_t mt = pass == kLinDw ? groups * ((s.n_out + c->bm - 1) / c->bm)
                                           : s.groups == 1 ? (s.rows + c->bm - 1) / c->bm : s.rows / c->bm + (groups + 1) / 2;
         const int64_t tiles = mt * ((n + c->bn - 1) / c->bn);
         for (int parts = 1; parts <= 16 && parts * 4 <= slices + 3; ++parts) {
             if (parts > 1 && tiles * parts > 4 * units) break;
-            const int64_t each = (slices + parts - 1) / parts, all = tiles * parts;
-            const double rest = static_cast<double>(all % units) / units;
-            const double round = all / units * c->full + (rest > 0.0 ? c->one + (c->full - c->one) * rest : 0.0);
-            double us = each * round;
-            if (parts > 1) us += 7.0 + values * 8.0 * parts / 4e6;
-            if (least < 0.0 || us < least) {
-                least = us;
-                best = Plan{c->shape, parts};
-            }
+            const int64_t all = tiles * parts, rounds = all / units;
+            const float rest = static_cast<float>(all - rounds * units) / units;
+            const float round = rounds * c->full + (rest > 0.0f ? c->one + (c->full - c->one) * rest : 0.0f);
+            float us = static_cast<float>((slices + parts - 1) / parts) * round;
+            us += extras * c->epilogue * (parts > 1 ? 0 : rounds + (rest > 0.0f ? 1 : 0));
+            if (parts > 1) us += 7.0f + values * parts * (8.0f / 4e6f);
+            if (best.us < 0.0f || us < best.us) best = Plan{c->shape, parts, us};
         }
     }
     return best;
@@ -127,8 +130,27 @@ bool few_rows(const moe_linear_shape& s) {
            groups * ((s.n_out + 127) / 128) < device_cus();
 }
 
+// dx, dW and db in one launch, on 128 x 128 (float32: 64 x 64) tiles, k not
+// split: where the longer of the two products, or both together spread over
+// the units, take less than one after the other by their own plans and the 6
+// us that a launch takes to begin and end (512 x 64 -> 128 in float32: 12 us
+// against 27, 300 x 512 -> 512 in bf16 17 against 31).
+bool backward_together(const moe_linear_shape& s, const Plan& dx, const Plan& dw) {
+    const bool f32 = s.act == MOE_F32;
+    const TileCost& c = f32 ? kF32Tiles[1] : kBf16Tiles[2];
+    const int64_t sk = f32 ? 16 : 32, groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
+    const int64_t nt = (s.n_in + c.bn - 1) / c.bn;
+    const float sx = static_cast<float>((s.n_out + sk - 1) / sk), sw = static_cast<float>((s.rows / groups + sk - 1) / sk);
+    const float tx = static_cast<float>((s.rows / c.bm + groups) * nt);
+    const float tw = static_cast<float>(s.groups) * ((s.n_out + c.bm - 1) / c.bm) * nt;
+    const float both = std::max(std::max(sx, sw) * c.one, (tx * sx + tw * sw) * c.full / device_cus());
+    return both < dx.us + dw.us + 6.0f;
+}
+
 struct LinLayout {
     size_t dz = 0, db = 0, part = 0, total = 0;
+    Plan fwd{0, 1, 0.0f}, dx{0, 1, 0.0f}, dw{0, 1, 0.0f};
+    bool together = false;  // dx, dW and db in one launch
 };
 LinLayout linear_layout(const moe_linear_shape& s, bool backward) {
     LinLayout L;
@@ -138,17 +160,19 @@ LinLayout linear_layout(const moe_linear_shape& s, bool backward) {
         off = align256(off + n);
         return at;
     };
-    auto parts = [&](int pass, size_t rows, size_t n) {
-        const Plan p = plan_of(s, pass);
-        return p.parts > 1 ? p.parts * rows * n * 4 : 0;
-    };
+    auto parts = [](const Plan& p, size_t rows, size_t n) { return p.parts > 1 ? p.parts * rows * n * 4 : 0; };
     const size_t R = static_cast<size_t>(s.rows), ni = s.n_in, no = s.n_out;
     if (backward) {
+        L.dx = plan_of(s, kLinDx);
+        L.dw = plan_of(s, kLinDw);
+        L.together = backward_together(s, L.dx, L.dw);
         L.dz = take(s.fn != MOE_FN_NONE ? R * no * act_size(s) : 0);
         L.db = take(static_cast<size_t>(linear_db_tiles(s.rows, s.groups)) * no * 4);
-        L.part = take(std::max(parts(kLinDx, R, ni), parts(kLinDw, s.groups * no, ni)));
+        // (a caller may ask for one of the two alone: room for its own plan)
+        L.part = take(std::max(parts(L.dx, R, ni), parts(L.dw, s.groups * no, ni)));
     } else {
-        L.part = take(parts(kLinForward, R, no));
+        L.fwd = plan_of(s, kLinForward);
+        L.part = take(parts(L.fwd, R, no));
     }
     L.total = off;
     return L;
@@ -165,16 +189,7 @@ int32_t check_saved(const moe_linear_shape& s, const void* saved, size_t saved_b
     return MOE_OK;
 }
 
-hipError_t run_product(const moe_linear_shape& s, int pass, LinearArgs a, void* ws, size_t part_at, hipStream_t st) {
-    if (pass == kLinForward && few_rows(s)) {
-        a.parts = 1;
-        // 16 columns a work-group where 32 would leave compute units idle
-        // (8-bit codes need 32: a block)
-        const int64_t blocks = static_cast<int64_t>(s.groups) * ((s.n_out + 31) / 32);
-        return launch_linear_rows(a, s.save != MOE_SAVE_INT8 && blocks < device_cus() ? 1 : 2, st);
-    }
-    const Plan p = plan_of(s, pass);
-    const bool f32 = s.act == MOE_F32;
+hipError_t run_product(const Plan& p, int pass, LinearArgs a, bool f32, void* ws, size_t part_at, hipStream_t st) {
     a.parts = p.parts;
     a.part_out = p.parts > 1 ? at<float>(ws, part_at) : nullptr;
     const hipError_t e = launch_linear_tile(pass, a, p.shape, f32, st);
@@ -213,7 +228,15 @@ int32_t linear_forward(const moe_linear_shape* s, const void* x, const int32_t* 
         a.scales = a.codes + rows8_scales_at(s->rows, s->n_out);
         a.n32 = rows8_stride(s->n_out);
     }
-    return hip_status(run_product(*s, kLinForward, a, ws, L.part, static_cast<hipStream_t>(stream)));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (few_rows(*s)) {
+        // 16 columns a work-group where 32 would leave compute units idle
+        // (8-bit codes need 32: a block)
+        a.parts = 1;
+        const int64_t blocks = std::min<int64_t>(s->groups, s->rows) * ((s->n_out + 31) / 32);
+        return hip_status(launch_linear_rows(a, s->save != MOE_SAVE_INT8 && blocks < device_cus() ? 1 : 2, st));
+    }
+    return hip_status(run_product(L.fwd, kLinForward, a, s->act == MOE_F32, ws, L.part, st));
 }
 
 int32_t linear_backward(const moe_linear_shape* s, const void* x, const int32_t* offsets, bool grouped, const void* w,
@@ -236,7 +259,9 @@ int32_t linear_backward(const moe_linear_shape* s, const void* x, const int32_t*
     // (without rows the offsets are not read: every group is empty)
     const int32_t* off = offsets;
     const uint8_t* dz = static_cast<const uint8_t*>(dy);
-    if (s->rows > 0 && (s->fn != MOE_FN_NONE || db != nullptr)) {
+    // without an activation dz is dy, and where that is short db sums it itself
+    const bool direct = s->fn == MOE_FN_NONE && s->rows <= 2048;
+    if (s->rows > 0 && (s->fn != MOE_FN_NONE || (db != nullptr && !direct))) {
         DzArgs d{};
         d.offsets = off;
         d.R = s->rows;
@@ -258,31 +283,38 @@ int32_t linear_backward(const moe_linear_shape* s, const void* x, const int32_t*
         d.db_part = db != nullptr ? at<float>(ws, L.db) : nullptr;
         MOE_TRY(hip_status(launch_linear_dz(d, f32, st)));
     }
-    LinearArgs a{};
-    a.a = dz;
-    a.offsets = off;
-    a.hdr = static_cast<uint32_t*>(ws);
-    a.R = s->rows;
-    a.G = s->groups;
-    a.fn = MOE_FN_NONE;
-    a.N = s->n_in;
-    if (dx != nullptr && s->rows > 0) {
-        a.b = static_cast<const uint8_t*>(w);
-        a.K = s->n_out;
-        a.out = static_cast<uint8_t*>(dx);
-        MOE_TRY(hip_status(run_product(*s, kLinDx, a, ws, L.part, st)));
+    LinearArgs x_args{}, w_args{};
+    x_args.a = w_args.a = dz;
+    x_args.offsets = w_args.offsets = off;
+    x_args.hdr = w_args.hdr = static_cast<uint32_t*>(ws);
+    x_args.R = w_args.R = s->rows;
+    x_args.G = w_args.G = s->groups;
+    x_args.N = w_args.N = s->n_in;
+    x_args.parts = w_args.parts = 1;
+    if (s->rows > 0 && dx != nullptr) {
+        x_args.b = static_cast<const uint8_t*>(w);
+        x_args.K = s->n_out;
+        x_args.out = static_cast<uint8_t*>(dx);
     }
     if (dw != nullptr) {
-        a.b = static_cast<const uint8_t*>(x);
-        a.M = s->n_out;
-        a.K = 0;
-        a.out = static_cast<uint8_t*>(dw);
-        a.out_f32 = s->grad == MOE_F32 ? 1 : 0;
-        MOE_TRY(hip_status(run_product(*s, kLinDw, a, ws, L.part, st)));
+        w_args.b = static_cast<const uint8_t*>(x);
+        w_args.M = s->n_out;
+        w_args.out = static_cast<uint8_t*>(dw);
+        w_args.out_f32 = s->grad == MOE_F32 ? 1 : 0;
     }
-    if (db != nullptr)
-        MOE_TRY(hip_status(launch_linear_db(off, s->rows, s->groups, s->n_out, at<float>(ws, L.db), db,
-                                            s->grad == MOE_F32, st)));
+    DbArgs b_args{};
+    b_args.offsets = off;
+    b_args.R = s->rows;
+    b_args.G = s->groups;
+    b_args.N = s->n_out;
+    b_args.part = direct ? nullptr : at<float>(ws, L.db);
+    b_args.dy = static_cast<const uint8_t*>(dy);
+    b_args.db = db;
+    b_args.db_f32 = s->grad == MOE_F32 ? 1 : 0;
+    if (L.together) return hip_status(launch_linear_backward(x_args, w_args, b_args, f32, st));
+    if (x_args.out != nullptr) MOE_TRY(hip_status(run_product(L.dx, kLinDx, x_args, f32, ws, L.part, st)));
+    if (w_args.out != nullptr) MOE_TRY(hip_status(run_product(L.dw, kLinDw, w_args, f32, ws, L.part, st)));
+    if (db != nullptr) MOE_TRY(hip_status(launch_linear_db(b_args, f32, st)));
     return MOE_OK;
 }
 

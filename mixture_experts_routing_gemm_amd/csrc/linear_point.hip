@@ -6,8 +6,6 @@
 
 namespace moe {
 
-// rows a work-group sums into one partial of the bias gradient
-constexpr int kDzRows = 128;
 constexpr int kDzCols = 256;
 
 struct DzArgs {
@@ -20,10 +18,10 @@ struct DzArgs {
     const uint8_t* scales;
     int64_t n32;
     uint8_t* dz;             // [R, N] (act) or NULL
-    float* db_part;          // [m-tiles of 128 rows][N] or NULL
+    float* db_part;          // [blocks of 32 rows of a group][N] or NULL
 };
 
-// A work-group takes 128 rows of one group and 256 columns: eight rows of 32
+// A work-group takes 32 rows of one group and 256 columns: eight rows of 32
 // lanes x 8 columns at a time. dz is rounded to the act type once (the
 // products that read it need that type); the bias gradient sums it before the
 // rounding, each thread its rows in order, then the eight threads of a column
@@ -84,27 +82,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs a) {
     }
 }
 
-// db[g][n] = the sum of the group's partials, four threads a column (each
-// every fourth partial, in order), then the four in order.
-template <typename TOut>
-__global__ __launch_bounds__(256) void linear_db_kernel(const int32_t* __restrict__ offsets, int64_t R, int G, int N,
-                                                        const float* __restrict__ part, TOut* __restrict__ db) {
-    __shared__ GroupWalk walk;
-    __shared__ float sums[4][64];
-    walk_groups(walk, offsets, R, G, kDzRows, nullptr);
-    const int g = blockIdx.y, col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-    float s = 0.0f;
-    if (col < N)
-        for (int t = walk.pre[g] + q; t < walk.pre[g + 1]; t += 4) s += part[static_cast<int64_t>(t) * N + col];
-    sums[q][threadIdx.x & 63] = s;
-    __syncthreads();
-    if (q == 0 && col < N) {
-        const float t = ((sums[0][threadIdx.x] + sums[1][threadIdx.x]) + sums[2][threadIdx.x]) + sums[3][threadIdx.x];
-        if constexpr (sizeof(TOut) == 4)
-            db[static_cast<int64_t>(g) * N + col] = t;
-        else
-            db[static_cast<int64_t>(g) * N + col] = f32_to_bf16(t);
-    }
+template <typename T>
+__global__ __launch_bounds__(512) void linear_db_kernel(DbArgs a) {
+    linear_db_block<T, 8>(a, blockIdx.y, blockIdx.x);
 }
 
 // The parts' sums of 32 x 32 values a wave, added part by part, then stored as
@@ -112,7 +92,7 @@ __global__ __launch_bounds__(256) void linear_db_kernel(const int32_t* __restric
 template <typename T, int PASS>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
     __shared__ GroupWalk walk;
-    if constexpr (PASS != kLinDw) walk_groups(walk, a.offsets, a.R, a.G, 1, a.hdr);
+    if constexpr (PASS != kLinDw) walk_groups(walk, a.offsets, a.R, a.G, 1, nullptr);
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
     const int nblk = (a.N + 31) / 32;
@@ -172,13 +152,12 @@ hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_linear_db(const int32_t* offsets, int64_t R, int G, int N, const float* part, void* db, bool f32,
-                            hipStream_t st) {
-    const dim3 grid((N + 63) / 64, G);
+hipError_t launch_linear_db(const DbArgs& a, bool f32, hipStream_t st) {
+    const dim3 grid((a.N + 63) / 64, a.G);
     if (f32)
-        linear_db_kernel<float><<<grid, 256, 0, st>>>(offsets, R, G, N, part, static_cast<float*>(db));
+        linear_db_kernel<float><<<grid, 512, 0, st>>>(a);
     else
-        linear_db_kernel<bf16_t><<<grid, 256, 0, st>>>(offsets, R, G, N, part, static_cast<bf16_t*>(db));
+        linear_db_kernel<bf16_t><<<grid, 512, 0, st>>>(a);
     return hipGetLastError();
 }
 

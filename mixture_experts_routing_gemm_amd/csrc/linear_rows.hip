@@ -133,7 +133,7 @@ linear_rows_kernel(LinearArgs a) {
     if (a.offsets != nullptr) {
         // the list of (row block, column block) is cut into eight runs, one
         // for each XCD: a group's columns share its rows of x in one L2
-        walk_groups(walk, a.offsets, a.R, a.G, kRowsBM, a.hdr);
+        walk_groups(walk, a.offsets, a.R, a.G, kRowsBM, blockIdx.x == 0 ? a.hdr : nullptr);
         const int total = __builtin_amdgcn_readfirstlane(walk.pre[a.G]) * a.ntn, xcd = blockIdx.x & 7;
         const auto eighth = [&](int i) { return (total >> 3) * i + ((total & 7) * i >> 3); };
         const int L = eighth(xcd) + static_cast<int>(blockIdx.x >> 3);

@@ -180,10 +180,9 @@ __device__ __forceinline__ void lin_mma(const u32x4& fb, const u32x4& fa, f32x16
     }
 }
 
+// The tiles of work-group `bid` of `nblk`.
 template <typename T, int PASS, class S>
-__global__ __launch_bounds__(lin_threads<S>())
-    __attribute__((amdgpu_waves_per_eu(lin_waves_per_simd<S>(), lin_waves_per_simd<S>())))
-void linear_tile_kernel(LinearArgs a) {
+__device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int nblk) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ GroupWalk walk;
     __shared__ GroupOrder order;
@@ -206,7 +205,7 @@ void linear_tile_kernel(LinearArgs a) {
     // stores of a full tile by a wave, at least (see the waits below)
     constexpr int kStores = kStage ? 4 * MB : 0;
 
-    walk_groups(walk, a.offsets, a.R, a.G, BM, a.hdr);
+    walk_groups(walk, a.offsets, a.R, a.G, BM, bid == 0 ? a.hdr : nullptr);
     if constexpr (PASS == kLinDw) order_groups(order, walk, a.G);
 
     const int tid = threadIdx.x;
@@ -242,10 +241,10 @@ void linear_tile_kernel(LinearArgs a) {
     auto next_source = [&](int list) {
         Source src;
         LinTile t;
-        bool more = lin_tile<PASS, BM, BN, SK>(a, walk, order, list, t);
+        bool more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
         ++list;
         while (more && t.k1 <= t.k0) {  // (a group without rows, or an empty part)
-            more = lin_tile<PASS, BM, BN, SK>(a, walk, order, list, t);
+            more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
             ++list;
         }
         src.list = list;
@@ -383,7 +382,7 @@ void linear_tile_kernel(LinearArgs a) {
     int relax = 0;  // steps left whose wait may leave the last tile's stores under way
     for (int it = 0;; ++it) {
         LinTile t;
-        if (!lin_tile<PASS, BM, BN, SK>(a, walk, order, it, t)) break;
+        if (!lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, it, t)) break;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -455,7 +454,44 @@ void linear_tile_kernel(LinearArgs a) {
     wait_vmcnt<0>();
 }
 
+template <typename T, int PASS, class S>
+__global__ __launch_bounds__(lin_threads<S>())
+    __attribute__((amdgpu_waves_per_eu(lin_waves_per_simd<S>(), lin_waves_per_simd<S>())))
+void linear_tile_kernel(LinearArgs a) {
+    linear_tiles<T, PASS, S>(a, blockIdx.x, gridDim.x);
+}
+
+// dx, dW and db of a small layer in one launch: none needs another's result,
+// and each alone leaves most units idle. Work-groups 0 .. nx-1 take dx's
+// tiles, nx .. nx+nw-1 dW's, the rest db's columns (nx and nw multiples of 8).
+template <typename T, class S>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(S::PER_CU, S::PER_CU)))
+void linear_backward_kernel(LinearArgs x, LinearArgs w, DbArgs d, int nx, int nw) {
+    static_assert(lin_threads<S>() == 256, "four waves");
+    const int b = blockIdx.x;
+    if (b < nx) {
+        linear_tiles<T, kLinDx, S>(x, b, nx);
+    } else if (b < nx + nw) {
+        linear_tiles<T, kLinDw, S>(w, b - nx, nw);
+    } else {
+        const int cbs = (d.N + 63) / 64, i = b - nx - nw;
+        linear_db_block<T, 4>(d, i / cbs, i % cbs);
+    }
+}
+
 namespace {
+
+// fills in the tile counts and gives the work-groups, or 0 for too many tiles
+template <int PASS, class S>
+unsigned tile_grid(LinearArgs& a) {
+    a.ntn = (a.N + S::BN - 1) / S::BN;
+    a.mtiles = PASS == kLinDw ? (a.M + S::BM - 1) / S::BM : 0;
+    const int64_t mt = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.mtiles : a.R / S::BM + a.G;
+    const int64_t tiles = mt * a.ntn * a.parts;
+    if (tiles >= (int64_t(1) << 30)) return 0;
+    const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(device_cus()) * S::PER_CU, tiles);
+    return static_cast<unsigned>(std::max<int64_t>(8, (blocks + 7) & ~int64_t(7)));
+}
 
 template <typename T, int PASS, class S>
 hipError_t launch(const LinearArgs& a0, hipStream_t st) {
@@ -464,14 +500,24 @@ hipError_t launch(const LinearArgs& a0, hipStream_t st) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (attr != hipSuccess) return attr;
     LinearArgs a = a0;
-    a.ntn = (a.N + S::BN - 1) / S::BN;
-    a.mtiles = PASS == kLinDw ? (a.M + S::BM - 1) / S::BM : 0;
-    const int64_t mt = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.mtiles : a.R / S::BM + a.G;
-    const int64_t tiles = mt * a.ntn * a.parts;
-    if (tiles >= (int64_t(1) << 30)) return hipErrorInvalidValue;
-    int64_t blocks = std::min<int64_t>(static_cast<int64_t>(device_cus()) * S::PER_CU, tiles);
-    blocks = std::max<int64_t>(8, (blocks + 7) & ~int64_t(7));
-    linear_tile_kernel<T, PASS, S><<<static_cast<unsigned>(blocks), lin_threads<S>(), ring, st>>>(a);
+    const unsigned blocks = tile_grid<PASS, S>(a);
+    if (blocks == 0) return hipErrorInvalidValue;
+    linear_tile_kernel<T, PASS, S><<<blocks, lin_threads<S>(), ring, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, class S>
+hipError_t launch_backward(const LinearArgs& x0, const LinearArgs& w0, const DbArgs& d, hipStream_t st) {
+    constexpr int ring = S::SLOTS * lin_slot<S>();
+    static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_backward_kernel<T, S>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (attr != hipSuccess) return attr;
+    LinearArgs x = x0, w = w0;
+    const unsigned nx = x.out != nullptr ? tile_grid<kLinDx, S>(x) : 0, nw = w.out != nullptr ? tile_grid<kLinDw, S>(w) : 0;
+    if ((x.out != nullptr && nx == 0) || (w.out != nullptr && nw == 0)) return hipErrorInvalidValue;
+    const unsigned nb = d.db != nullptr ? static_cast<unsigned>(d.G) * ((d.N + 63) / 64) : 0;
+    if (nx + nw + nb == 0) return hipSuccess;
+    linear_backward_kernel<T, S><<<nx + nw + nb, 256, ring, st>>>(x, w, d, static_cast<int>(nx), static_cast<int>(nw));
     return hipGetLastError();
 }
 
@@ -490,6 +536,12 @@ hipError_t launch_pass(const LinearArgs& a, int shape, bool f32, hipStream_t st)
 }
 
 }  // namespace
+
+// dx, dW and db together (out or db NULL: not computed), 128 x 128 tiles in
+// bf16, 64 x 64 in float32, k not split
+hipError_t launch_linear_backward(const LinearArgs& x, const LinearArgs& w, const DbArgs& d, bool f32, hipStream_t st) {
+    return f32 ? launch_backward<float, LinTiny>(x, w, d, st) : launch_backward<bf16_t, LinMid>(x, w, d, st);
+}
 
 // shape: a LinTileShape (float32: Mid or Tiny; bf16: the others; dW: not Small)
 hipError_t launch_linear_tile(int pass, const LinearArgs& a, int shape, bool f32, hipStream_t st) {

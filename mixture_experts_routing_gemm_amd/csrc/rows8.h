@@ -8,7 +8,8 @@
 // power of two so that v / 2^e is exact before the one rounding and a value
 // read back, 7 significant bits times 2^e, is exact in bf16 as in float32:
 // what a kernel multiplies is what the format holds. A block with an infinity
-// or a NaN gets scale byte 255 and codes 0 and reads back as NaN.
+// or a NaN gets scale byte 255 and reads back as NaN, whatever
+// its codes.
 //
 // A buffer of `rows` rows of n values: the codes [rows, n32] (n32 = n rounded
 // up to 32; the padding's codes are 0), rounded up to 256 bytes, then the
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint32_t rows8_scale(uint32_t amax_bits) {
     return q == 255 ? 255u : static_cast<uint32_t>(b < 1 ? 1 : b);
 }
 // 2^-e, by which a value is multiplied before its rounding (0 for a block
-// that is not finite: its codes are 0); e >= -126 and e <= 121
+// that is not finite); e >= -126 and e <= 121
 __device__ __forceinline__ float rows8_inverse(uint32_t scale) {
     return scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
 }
@@ -49,14 +50,17 @@ __device__ __forceinline__ float rows8_inverse(uint32_t scale) {
 __device__ __forceinline__ float rows8_step(uint32_t scale) {
     return scale == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(scale << 23);
 }
-// (a block that is not finite: inverse 0, and an infinity times 0 is a NaN,
-// which converts to 0)
-__device__ __forceinline__ uint32_t rows8_code(float v, float inverse) {
-    return static_cast<uint32_t>(static_cast<int>(__builtin_rintf(v * inverse))) & 0xffu;
-}
+// Four codes as the bytes of a word. v * inverse is exact, so adding 1.5 * 2^23
+// (whose last bit is worth 1) in one fused step rounds it to the nearest whole
+// number, ties to even, and leaves it in two's complement in the low byte.
 __device__ __forceinline__ uint32_t rows8_code4(float a, float b, float c, float d, float inverse) {
-    return rows8_code(a, inverse) | (rows8_code(b, inverse) << 8) | (rows8_code(c, inverse) << 16) |
-           (rows8_code(d, inverse) << 24);
+    const uint32_t qa = __float_as_uint(__builtin_fmaf(a, inverse, 12582912.0f));
+    const uint32_t qb = __float_as_uint(__builtin_fmaf(b, inverse, 12582912.0f));
+    const uint32_t qc = __float_as_uint(__builtin_fmaf(c, inverse, 12582912.0f));
+    const uint32_t qd = __float_as_uint(__builtin_fmaf(d, inverse, 12582912.0f));
+    // v_perm_b32: bytes 0..3 of the second operand, 4..7 of the first
+    const uint32_t ab = __builtin_amdgcn_perm(qb, qa, 0x0c0c0400u), cd = __builtin_amdgcn_perm(qd, qc, 0x04000c0cu);
+    return ab | cd;
 }
 __device__ __forceinline__ float rows8_value(uint32_t word, int i, float step) {
     return static_cast<float>(static_cast<int8_t>((word >> (8 * i)) & 0xffu)) * step;
