@@ -423,7 +423,8 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
     if constexpr (PASS == kLinDw) {
         const int per_group = a.mtiles * a.ntn;
         const int total = a.G * per_group * a.parts;
-        const int L = ((c >> 2) * 8 + xcd) * 4 + (c & 3);
+        // (one at a time where four would leave XCDs with more than others)
+        const int L = total % 32 == 0 || total >= 4 * nblk ? ((c >> 2) * 8 + xcd) * 4 + (c & 3) : c * 8 + xcd;
         if (L >= total) return false;
         const int gp = L / per_group;
         const int rank = gp / a.parts;

@@ -23,7 +23,7 @@ struct DzArgs {
 
 int device_cus();
 hipError_t launch_linear_tile(int pass, const LinearArgs& a, int shape, bool f32, hipStream_t st);
-hipError_t launch_linear_rows(const LinearArgs& a, int fb, hipStream_t st);
+hipError_t launch_linear_rows(const LinearArgs& a, int fb, bool f32, hipStream_t st);
 hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st);
 int64_t linear_db_tiles(int64_t R, int G);
 hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st);
@@ -126,7 +126,7 @@ Plan plan_of(const moe_linear_shape& s, int pass) {
 // 4 rows, 2048 -> 1408: 16 against 19, of 16 rows 20 against 19).
 bool few_rows(const moe_linear_shape& s) {
     const int64_t groups = std::min<int64_t>(s.groups, s.rows);
-    return s.act == MOE_BF16 && s.rows <= s.groups * int64_t(s.groups == 1 ? 32 : 8) &&
+    return s.rows <= s.groups * int64_t(s.groups == 1 ? 32 : 8) &&
            groups * ((s.n_out + 127) / 128) < device_cus();
 }
 
@@ -234,7 +234,8 @@ int32_t linear_forward(const moe_linear_shape* s, const void* x, const int32_t* 
         // (8-bit codes need 32: a block)
         a.parts = 1;
         const int64_t blocks = std::min<int64_t>(s->groups, s->rows) * ((s->n_out + 31) / 32);
-        return hip_status(launch_linear_rows(a, s->save != MOE_SAVE_INT8 && blocks < device_cus() ? 1 : 2, st));
+        return hip_status(launch_linear_rows(a, s->save != MOE_SAVE_INT8 && blocks < device_cus() ? 1 : 2,
+                                             s->act == MOE_F32, st));
     }
     return hip_status(run_product(L.fwd, kLinForward, a, s->act == MOE_F32, ws, L.part, st));
 }
