@@ -103,7 +103,8 @@ typedef enum {
     MOE_STAGE_FFN_BACKWARD = 6,
     MOE_STAGE_FORWARD_FP8W = 7,
     MOE_STAGE_LINEAR = 8,          /* moe_linear_workspace_bytes */
-    MOE_STAGE_LINEAR_BACKWARD = 9  /* moe_linear_workspace_bytes */
+    MOE_STAGE_LINEAR_BACKWARD = 9, /* moe_linear_workspace_bytes */
+    MOE_STAGE_FFN_BACKWARD8 = 10
 } moe_stage;
 
 /* the activation of a linear layer: gelu(z) = z Phi(z) (the exact form, Phi
@@ -138,7 +139,7 @@ typedef struct {
 } moe_shape;
 
 /* A linear layer over rows sorted by group (moe_grouped_linear), or with one
- * weight matrix (moe_linear: groups = 1). Limits: 0 <= rows < 2^31, n_in and
+ * weight matrix (moe_linear: groups = 1). Limits: 0 <= rows <= 2^31 - 4096, n_in and
  * n_out at most 2^20 and multiples of 8 (act = MOE_BF16) or 4 (MOE_F32), so
  * that every row moves as 16-byte pieces; 1 <= groups <= 256. */
 typedef struct {
@@ -403,15 +404,16 @@ int32_t moe_grouped_ffn_backward_saved(const moe_shape *s, const void *x_perm,
  *
  * moe_ffn_saved8_bytes: bytes of the buffer, or 0 when the shape is not
  *  supported: act must be MOE_BF16, the shape on the persistent tiles
- *  (d % 256 == 0, h % 128 == 0), and x, the weights W1 with W3 and the hidden
- *  rows' gradients [rows, 2h] each below 4 GiB. The buffer holds four rows8
+ *  (d % 256 == 0, h % 128 == 0; rows of d and of 2h values, and W1, each below
+ *  4 GiB). The buffer holds four rows8
  *  buffers: a and b of the routed rows [T*k, h], a and b of the shared
  *  experts' token rows [T, S*h] (nothing for S = 0).
  * moe_grouped_ffn_save8: moe_grouped_ffn (same arguments and results) that
  *  also writes a and b into `saved8` (caller-owned, 256-byte aligned).
  * moe_grouped_ffn_backward_saved8: as moe_grouped_ffn_backward, from
  *  `saved8`; dw1, dw3, dw2 are of type `grad`, MOE_F32 or MOE_BF16 (summed in
- *  float32 and rounded once). ws: MOE_STAGE_FFN_BACKWARD bytes. T = 0 only
+ *  float32 and rounded once). ws: MOE_STAGE_FFN_BACKWARD8 bytes (hid and the
+ *  gradients of a and b; no transposed weights). T = 0 only
  *  zeroes the weight gradients.
  * Errors as for moe_grouped_ffn_save and moe_grouped_ffn_backward_saved;
  * MOE_ERR_UNSUPPORTED for another `grad`.

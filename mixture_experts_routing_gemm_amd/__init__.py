@@ -21,7 +21,7 @@ from ._binding import (  # noqa: F401
     moe_gate_topk, moe_get_device_error, moe_grouped_ffn, moe_grouped_ffn_backward, moe_shape,
     moe_ffn_saved_bytes, alloc_saved, moe_grouped_ffn_save, moe_grouped_ffn_backward_saved,
     MOE_FN_GELU, MOE_FN_NONE, MOE_FN_RELU, MOE_FN_SILU, MOE_SAVE_ACT, MOE_SAVE_INT8, MOE_SAVE_NONE,
-    STAGE_LINEAR, STAGE_LINEAR_BACKWARD, alloc_linear_saved, alloc_linear_workspace, alloc_rows8,
+    STAGE_LINEAR, STAGE_LINEAR_BACKWARD, STAGE_FFN_BACKWARD8, alloc_linear_saved, alloc_linear_workspace, alloc_rows8,
     make_linear_shape, moe_grouped_linear, moe_grouped_linear_backward, moe_linear, moe_linear_backward,
     moe_linear_saved_bytes, moe_linear_shape, moe_linear_workspace_bytes, moe_pack_rows8, moe_rows8_bytes,
     moe_unpack_rows8, moe_ffn_saved8_bytes, alloc_saved8, moe_grouped_ffn_save8,

@@ -32,6 +32,7 @@ STAGE_FFN_BACKWARD = 6
 STAGE_FORWARD_FP8W = 7
 STAGE_LINEAR = 8
 STAGE_LINEAR_BACKWARD = 9
+STAGE_FFN_BACKWARD8 = 10
 FP8W_KERNELS = ["gate_topk", "dispatch_rank", "dispatch_scan", "dispatch_permute_fp8", "ffn_plan",
                 "ffn_up", "ffn_hidden_quant", "ffn_down", "combine"]
 

@@ -515,7 +515,7 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
                                 const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh,
                                 int32_t* plan_f, int32_t* plan_dh, void* h_r, void* h_s, void* a_r,
                                 void* b_r, void* a_s, void* b_s, void* dd_r, void* dd_s,
-                                hipStream_t st, const Marks* mk, bool recompute, const void* saved8);
+                                hipStream_t st, const Marks* mk, bool recompute);
 bool wgrad_supported(const moe_shape& s);
 size_t wgrad_ws_bytes(const moe_shape& s);
 hipError_t launch_ffn_wgrad(const moe_shape& s, const int32_t* offsets, const void* dd_r,
@@ -608,17 +608,94 @@ SavedLayout saved_layout(const moe_shape& s) {
     return L;
 }
 
+// The backward from a and b in 8 bits. dh and dx are the linear layers' tile
+// kernel (linear_tile.hip), which reads W2, W1 and W3 as they lie: no
+// transposed weights. Workspace: hid and [da | db] of every row, then the
+// weight-gradient plan.
+struct Bwd8Layout {
+    bool wg;
+    size_t h_r, h_s, dd_r, dd_s, wgq, bytes;
+};
+Bwd8Layout bwd8_layout(const moe_shape& s) {
+    Bwd8Layout L{};
+    const size_t R = static_cast<size_t>(s.T) * s.k, TS = static_cast<size_t>(s.T) * s.S, h = s.h;
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off = (off + n + 255) & ~static_cast<size_t>(255);
+        return at;
+    };
+    L.h_r = take(R * h * 2);
+    L.h_s = take(TS * h * 2);
+    L.dd_r = take(R * 2 * h * 2);
+    L.dd_s = take(TS * 2 * h * 2);
+    L.wg = wgrad_supported(s);
+    L.wgq = take(wgrad_ws_bytes(s));
+    L.bytes = off;
+    return L;
+}
+
+hipError_t launch_ffn_dh8(const moe_shape& s, const int32_t* offsets, const void* w2, const void* dy_perm,
+                          const void* dy_sh, const void* saved8, void* h_r, void* h_s, void* dd_r, void* dd_s,
+                          hipStream_t st);
+hipError_t launch_ffn_dx2(const moe_shape& s, const int32_t* offsets, const void* w1, const void* w3, const void* dd_r,
+                          const void* dd_s, void* dx_perm, void* dx_sh, hipStream_t st);
+
+hipError_t launch_ffn_backward8(const moe_shape& s, const void* x_perm, const float* qparams, const int32_t* offsets,
+                                const void* x, const void* w1, const void* w3, const void* w2, const void* saved8,
+                                const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh, void* dw1, void* dw3,
+                                void* dw2, bool dw_bf16, void* ws, hipStream_t st) {
+    const Bwd8Layout L = bwd8_layout(s);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    hipError_t e = launch_ffn_dh8(s, offsets, w2, dy_perm, dy_sh, saved8, w + L.h_r, w + L.h_s, w + L.dd_r, w + L.dd_s, st);
+    if (e != hipSuccess) return e;
+    e = launch_ffn_dx2(s, offsets, w1, w3, w + L.dd_r, w + L.dd_s, dx_perm, dx_sh, st);
+    if (e != hipSuccess) return e;
+    if (L.wg)
+        return launch_ffn_wgrad(s, offsets, w + L.dd_r, w + L.dd_s, x_perm, x, dy_perm, dy_sh, w + L.h_r, w + L.h_s, dw1,
+                                dw3, dw2, dw_bf16, w + L.wgq, st);
+    // fp8 rows
+    BwdArgs a{};
+    a.offsets = offsets;
+    a.T = s.T;
+    a.E = s.E;
+    a.S = s.S;
+    a.d = s.d;
+    a.h = a.hs = s.h;
+    a.fp8 = s.dispatch == MOE_FP8_E4M3 ? 1 : 0;
+    a.x_perm = static_cast<const uint8_t*>(x_perm);
+    a.qparams = qparams;
+    a.x = static_cast<const uint8_t*>(x);
+    a.dy_perm = static_cast<const uint8_t*>(dy_perm);
+    a.dy_sh = static_cast<const uint8_t*>(dy_sh);
+    a.h_r = w + L.h_r;
+    a.h_s = w + L.h_s;
+    a.da_r = w + L.dd_r;
+    a.db_r = a.da_r + static_cast<size_t>(s.h) * 2;
+    a.da_s = w + L.dd_s;
+    a.db_s = a.da_s + static_cast<size_t>(s.h) * 2;
+    a.dw1 = dw1;
+    a.dw3 = dw3;
+    a.dw2 = dw2;
+    a.dw_bf16 = dw_bf16 ? 1 : 0;
+    a.dd_ld = 2 * s.h;
+    a.dd_lds = 2 * s.S * s.h;
+    a.dd_gs = 2 * s.h;
+    a.tpg = ((s.d + kTB - 1) / kTB) * ((s.h + kTB - 1) / kTB);
+    const int64_t nblk = 3 * static_cast<int64_t>(s.E + s.S) * a.tpg;
+    ffn_bwd_wgrad_kernel<<<static_cast<unsigned>(nblk), kBwdThreads, kBwdLds, st>>>(a);
+    return hipGetLastError();
+}
+
+size_t ffn_backward8_ws_bytes(const moe_shape& s) { return bwd8_layout(s).bytes; }
+
 hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const float* qparams,
                                const int32_t* offsets, const void* x, const void* w1,
                                const void* w3, const void* w2, const void* dy_perm,
-                               const void* dy_sh, void* dx_perm, void* dx_sh, void* dw1,
-                               void* dw3, void* dw2, void* ws, hipStream_t st,
-                               const Marks* mk, const void* saved, const void* saved8,
-                               bool dw_bf16) {
+                               const void* dy_sh, void* dx_perm, void* dx_sh, float* dw1,
+                               float* dw3, float* dw2, void* ws, hipStream_t st,
+                               const Marks* mk, const void* saved) {
     const BwdLayout L = bwd_layout(s);
-    // (a and b in 8 bits: the dh kernel of the persistent path reads them and
-    // writes hid into the workspace)
-    if (saved8 != nullptr && !L.big) return hipErrorInvalidValue;
     uint8_t* w = static_cast<uint8_t*>(ws);
     // a, b and hid: saved by the forward, or recomputed into the workspace
     const SavedLayout SL = saved_layout(s);
@@ -661,7 +738,6 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
     a.dw1 = dw1;
     a.dw3 = dw3;
     a.dw2 = dw2;
-    a.dw_bf16 = dw_bf16 ? 1 : 0;
     hipError_t e;
     mark(mk);
     if (L.big) {
@@ -681,7 +757,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
                                  dx_perm, dx_sh, reinterpret_cast<int32_t*>(w + L.plan),
                                  reinterpret_cast<int32_t*>(w + L.plan_dh), p_h_r, p_h_s,
                                  p_a_r, p_b_r, p_a_s, p_b_s, w + L.da_r, w + L.da_s,
-                                 st, mk, sv == nullptr && saved8 == nullptr, saved8);
+                                 st, mk, sv == nullptr);
         if (e != hipSuccess) return e;
         // the weight gradients read [da | db] rows and the routed m-tile
         // prefix of 128-row tiles is not needed by them
@@ -716,7 +792,7 @@ hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const flo
     }
     if (L.big && L.wg) {
         e = launch_ffn_wgrad(s, offsets, w + L.da_r, w + L.da_s, x_perm, x, dy_perm, dy_sh, p_h_r,
-                             p_h_s, dw1, dw3, dw2, dw_bf16, w + L.wgq, st);
+                             p_h_s, dw1, dw3, dw2, false, w + L.wgq, st);
         if (e != hipSuccess) return e;
         mark(mk);
         return hipSuccess;

@@ -36,18 +36,15 @@ namespace moe {
 // kModeUp / kModeUpFp8 that also store the pre-activations a and b;
 // kModeDh computes dhid = dy W2 (K = d, from the transposed W2, one weight
 // row per output column) with the SwiGLU backward in its epilogue.
-// kModeUpSave8, kModeUpFp8Save8 and kModeDh8 are the same with a and b kept in
-// 8 bits (rows8.h); kModeDh8 also writes the hidden rows again, from the a and
-// b that it reads, for the weight gradient of W2.
+// kModeUpSave8 and kModeUpFp8Save8 are the same with a and b kept in 8 bits
+// (rows8.h; their backward's products are those of the linear layers).
 enum {
     kModeUp = 0, kModeUpFp8 = 1, kModeDown = 2, kModeUpF8W = 3, kModeDownF8W = 4,
-    kModeUpSave = 5, kModeUpFp8Save = 6, kModeDh = 7, kModeUpSave8 = 8, kModeUpFp8Save8 = 9,
-    kModeDh8 = 10
+    kModeUpSave = 5, kModeUpFp8Save = 6, kModeDh = 7, kModeUpSave8 = 8, kModeUpFp8Save8 = 9
 };
 constexpr bool is_down(int m) { return m == kModeDown || m == kModeDownF8W; }
 constexpr bool is_fp8rows(int m) { return m == kModeUpFp8 || m == kModeUpFp8Save || m == kModeUpFp8Save8; }
 constexpr bool is_save8(int m) { return m == kModeUpSave8 || m == kModeUpFp8Save8; }
-constexpr bool is_dh(int m) { return m == kModeDh || m == kModeDh8; }
 constexpr bool is_save(int m) { return m == kModeUpSave || m == kModeUpFp8Save; }
 constexpr bool is_f8w(int m) { return m == kModeUpF8W || m == kModeDownF8W; }
 // bf16 operands in both roles: the upper row of waves (0-3) issues every
@@ -97,13 +94,11 @@ struct GemmArgs {
     uint8_t* pre_a_shared;
     uint8_t* pre_b_shared;
     // the 8-bit modes: pre_* are then codes, and these their scale bytes, a row
-    // of h / 32 (routed) or S h / 32 (shared); dh: the hidden rows, laid out as H
+    // of h / 32 (routed) or S h / 32 (shared)
     uint8_t* sc_a_routed;
     uint8_t* sc_b_routed;
     uint8_t* sc_a_shared;
     uint8_t* sc_b_shared;
-    uint8_t* hid_routed;
-    uint8_t* hid_shared;
     // fp8-weight modes: (scale, centre) of the shared experts' token rows
     // [T, 2]; the weight scales s1 | qsum1 | s3 | qsum3 [G, h] | s2 [G, d];
     // the hidden rows' scales, routed [rows] and shared [T]
@@ -601,7 +596,7 @@ __device__ __forceinline__ void tile_sources(const GemmArgs& a, const TileInfo& 
             if (is_down(MODE)) {
                 const int n = ti.nt * kBigBN + br;
                 out[i] = static_cast<uint32_t>(n) * a.h * eb + c * 16;
-            } else if (is_dh(MODE)) {
+            } else if (MODE == kModeDh) {
                 // the transposed W2 [G, h, d]: weight row n is hidden feature n
                 // (rows past h, in a last partial n-tile, are read and unused)
                 const int n = ti.nt * kBigBN + br;
@@ -1169,35 +1164,7 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                 }
             }
         };
-        // dh from 8 bits: the codes of the same values, a word of four, and the
-        // step of each 32-value block (a block is the 32 columns of one nb)
-        uint32_t dh_cd[NB][4][2];
-        float dh_st[NB][2];
-        auto dh_load8 = [&](int mbi) {
-            const int rr = cur.m0 + wm * kBigWM + mbi * 32 + lr;
-            const int sg = cur.shared ? cur.g - a.E : 0;
-            const int lpre = cur.shared ? a.S * a.h : a.h;
-            const int64_t prow = static_cast<int64_t>(cur.row_base) + min(rr, cur.nrows - 1);
-            const uint8_t* ca = (cur.shared ? a.pre_a_shared : a.pre_a_routed) + prow * lpre + sg * a.h;
-            const uint8_t* cb = (cur.shared ? a.pre_b_shared : a.pre_b_routed) + prow * lpre + sg * a.h;
-            const uint8_t* sa = (cur.shared ? a.sc_a_shared : a.sc_a_routed) + (prow * lpre + sg * a.h) / kRows8Block;
-            const uint8_t* sb = (cur.shared ? a.sc_b_shared : a.sc_b_routed) + (prow * lpre + sg * a.h) / kRows8Block;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int col = cur.nt * kBigBN + wn * kBigWN + nb * 32;
-                const bool in = col < a.h;
-                dh_st[nb][0] = rows8_step(in ? sa[col / kRows8Block] : 0u);
-                dh_st[nb][1] = rows8_step(in ? sb[col / kRows8Block] : 0u);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int f = col + 8 * q + 4 * lg;
-                    dh_cd[nb][q][0] = in ? *reinterpret_cast<const uint32_t*>(ca + f) : 0u;
-                    dh_cd[nb][q][1] = in ? *reinterpret_cast<const uint32_t*>(cb + f) : 0u;
-                }
-            }
-        };
         if constexpr (MODE == kModeDh) dh_load(0, 0);
-        if constexpr (MODE == kModeDh8) dh_load8(0);
         if constexpr (kStage) {
             ring_barrier();
             stage = lds + 3 * kBigSlot + wave * 4096;
@@ -1264,7 +1231,7 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                         __builtin_amdgcn_raw_buffer_store_b128(
                             v[i], orsrc, obase + static_cast<uint32_t>(mb * 32 + 8 * i) * orow, 0, 2);
                 }
-            } else if constexpr (is_dh(MODE)) {
+            } else if constexpr (MODE == kModeDh) {
                 // dhid -> da = dhid b s (1 + a (1 - s)), db = dhid silu(a)
                 // (s = sigmoid(a)) from the recomputed a, b; da and db of a
                 // group's row side by side: [da | db], 2h values per group
@@ -1272,32 +1239,18 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                 const int lpre = cur.shared ? a.S * a.h : a.h;
                 const int lout = 2 * lpre;
                 const int cb = 0;
-                if (mb > 0) {
-                    if constexpr (MODE == kModeDh8) dh_load8(mb);
-                    else dh_load(mb, 0);
-                }
+                if (mb > 0) dh_load(mb, 0);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     const int col = cur.nt * kBigBN + wn * kBigWN + nb * 32;
                     if (col >= a.h) continue;  // a last partial n-tile (h % 256 == 128)
-                    uint32_t wa_[4][2], wb_[4][2], wh_[4][2];
+                    uint32_t wa_[4][2], wb_[4][2];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        float av[4], bv[4];
-                        if constexpr (MODE == kModeDh8) {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                av[u] = rows8_value(dh_cd[nb][q][0], u, dh_st[nb][0]);
-                                bv[u] = rows8_value(dh_cd[nb][q][1], u, dh_st[nb][1]);
-                            }
-                            wh_[q][0] = pack_bf16x2(silu(av[0]) * bv[0], silu(av[1]) * bv[1]);
-                            wh_[q][1] = pack_bf16x2(silu(av[2]) * bv[2], silu(av[3]) * bv[3]);
-                        } else {
-                            const uint2 av4 = dh_ab[cb][nb][q][0];
-                            const uint2 bv4 = dh_ab[cb][nb][q][1];
-                            av[0] = bf16_lo(av4.x), av[1] = bf16_hi(av4.x), av[2] = bf16_lo(av4.y), av[3] = bf16_hi(av4.y);
-                            bv[0] = bf16_lo(bv4.x), bv[1] = bf16_hi(bv4.x), bv[2] = bf16_lo(bv4.y), bv[3] = bf16_hi(bv4.y);
-                        }
+                        const uint2 av4 = dh_ab[cb][nb][q][0];
+                        const uint2 bv4 = dh_ab[cb][nb][q][1];
+                        const float av[4] = {bf16_lo(av4.x), bf16_hi(av4.x), bf16_lo(av4.y), bf16_hi(av4.y)};
+                        const float bv[4] = {bf16_lo(bv4.x), bf16_hi(bv4.x), bf16_lo(bv4.y), bf16_hi(bv4.y)};
                         float da[4], db[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
@@ -1314,10 +1267,6 @@ __device__ __forceinline__ void persistent_gemm(const GemmArgs& a) {
                     bf16_t* orow = out + row * lout + sg * 2 * a.h + col;
                     store_groups(orow, wa_, ok);
                     store_groups(orow + a.h, wb_, ok);
-                    if constexpr (MODE == kModeDh8) {
-                        bf16_t* hid = reinterpret_cast<bf16_t*>(cur.shared ? a.hid_shared : a.hid_routed);
-                        store_groups(hid + row * lpre + sg * a.h + col, wh_, ok);
-                    }
                 }
             } else {
                 const int ldo = cur.shared ? a.S * a.h : a.h;
@@ -1930,6 +1879,12 @@ bool ffn_backward_big(const moe_shape& s) {
            2 * wbytes < (uint64_t(1) << 32);
 }
 
+// (the forward's tiles; the weight gradients' 32-bit offsets)
+bool ffn_saved8_supported(const moe_shape& s) {
+    const uint64_t rows = static_cast<uint64_t>(s.T) * (s.k + s.S);
+    return use_big_tiles(s) && rows * 2 * s.h * 2 < (uint64_t(1) << 32);
+}
+
 size_t ffn_plan_bytes_dh(const moe_shape& s) {
     return plan_layout(s, (s.h + kBigBN - 1) / kBigBN, s.d / kBigBN).bytes;
 }
@@ -1940,7 +1895,7 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
                                 const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh,
                                 int32_t* plan_f, int32_t* plan_dh, void* h_r, void* h_s, void* a_r,
                                 void* b_r, void* a_s, void* b_s, void* dd_r, void* dd_s,
-                                hipStream_t st, const Marks* mk, bool recompute, const void* saved8) {
+                                hipStream_t st, const Marks* mk, bool recompute) {
     const PlanLayout pf = plan_layout(s);
     const PlanLayout pd = plan_layout(s, (s.h + kBigBN - 1) / kBigBN, s.d / kBigBN);
     int32_t* cf = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(plan_f) + pf.counters);
@@ -2005,14 +1960,7 @@ hipError_t launch_ffn_bwd_gemms(const moe_shape& s, const void* x_perm, const fl
     a.out_routed = static_cast<uint8_t*>(dd_r);
     a.out_shared = static_cast<uint8_t*>(dd_s);
     a.ntn = pd.ntn_up;
-    if (saved8 != nullptr) {
-        set_saved8(s, a, static_cast<uint8_t*>(const_cast<void*>(saved8)));
-        a.hid_routed = static_cast<uint8_t*>(h_r);
-        a.hid_shared = static_cast<uint8_t*>(h_s);
-        err = launch_persistent<kModeDh8>(a, max_mtiles(s, kBigBM, false), st);
-    } else {
-        err = launch_persistent<kModeDh>(a, max_mtiles(s, kBigBM, false), st);
-    }
+    err = launch_persistent<kModeDh>(a, max_mtiles(s, kBigBM, false), st);
     mark(mk);
     if (err != hipSuccess) return err;
     // dx = [da | db] W13T^T: the down-projection with 2h hidden values

@@ -21,7 +21,11 @@ namespace moe {
 
 constexpr int kMaxGroups = 256;
 
-enum LinearPass { kLinForward = 0, kLinDx = 1, kLinDw = 2 };
+// For the SwiGLU experts' backward from 8 bits: kLinDh8 is dx of the
+// down-projection, dhid = dy W2, with the SwiGLU backward in its epilogue;
+// kLinDx2 is dx of the up-projections, [da | db] [W1; W3], k running over
+// segments of W1 and W3 in turn.
+enum LinearPass { kLinForward = 0, kLinDx = 1, kLinDw = 2, kLinDh8 = 3, kLinDx2 = 4 };
 // output tiles: 256 x 256, 256 x 128, 128 x 128, 64 x 128, 64 x 64
 enum LinTileShape { kLinTileBig = 0, kLinTileHalf = 1, kLinTileMid = 2, kLinTileSmall = 3, kLinTileTiny = 4 };
 
@@ -48,6 +52,21 @@ struct LinearArgs {
     // part_out [parts][rows][N] (rows: R, or G * M for dW), joined later
     float* part_out;
     int parts;
+    // every group holds all R rows (the shared experts); without offsets only
+    int same_rows;
+    // kLinDh8: a and b in 8 bits and hid, rows of ldp values, group g's at
+    // column g N (same_rows) or 0; out: [da | db] rows of 2 ldp values, group
+    // g's at column 2 g N or 0
+    const uint8_t* ca;
+    const uint8_t* cb;
+    const uint8_t* sa;
+    const uint8_t* sb;
+    uint8_t* hid;
+    int ldp;
+    // kLinDx2: b is W1 and b2 W3, segments of seg k values: W1 of the group,
+    // its W3, then the next group's
+    const uint8_t* b2;
+    int seg;
 };
 
 // ------------------------------------------------------------ functions --
@@ -121,11 +140,10 @@ __device__ __forceinline__ void walk_groups(GroupWalk& w, const int32_t* __restr
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         if (offsets == nullptr) {
-            if (lane == 0) {
-                w.off[0] = 0;
-                w.off[1] = R32;
-                w.pre[0] = 0;
-                w.pre[1] = (R32 + bm - 1) / bm;
+            // (more than one group: groups that each hold all R rows)
+            for (int g = lane; g <= G; g += 64) {
+                w.off[g] = g * R32;
+                w.pre[g] = g * ((R32 + bm - 1) / bm);
             }
         } else {
             // lane i holds entries per*i .. per*i + per-1 of the G + 1 offsets
@@ -451,7 +469,7 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
         t.m0 = m * BM;
         t.c0 = nt * BN;
         t.rows = w.off[t.g + 1] - w.off[t.g];
-        t.row0 = w.off[t.g];
+        t.row0 = a.same_rows ? 0 : w.off[t.g];
         part_range<SK>(0, a.K, t.part, a.parts, t.k0, t.k1);
     }
     // (the same for every lane by construction)
@@ -477,10 +495,10 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w
 __device__ __forceinline__ uint8_t* stage_at(uint8_t* stage, int row, int chunk) {
     return stage + row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
 }
-// the staged 32 x 64 block at rows m .., columns c .. of a [.., N] bf16 array
-// whose row 0 is the group's first; the rows below `rows`, columns below N
-__device__ __forceinline__ void stage_out(const uint8_t* stage, uint8_t* out, int64_t row0, int rows, int N, int m, int c,
-                                          int lane) {
+// the staged 32 x 64 block at rows m .. (below `rows`, counted from row0) and
+// columns c .. (below `cols`) of a bf16 array with ld values a row
+__device__ __forceinline__ void stage_out(const uint8_t* stage, uint8_t* out, int64_t row0, int rows, int ld, int cols,
+                                          int m, int c, int lane) {
     u32x4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = load16(stage_at(const_cast<uint8_t*>(stage), 8 * i + (lane >> 3), lane & 7));
@@ -488,8 +506,8 @@ __device__ __forceinline__ void stage_out(const uint8_t* stage, uint8_t* out, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = m + 8 * i + (lane >> 3);
-        if (r < rows && col < N)
-            *(__attribute__((address_space(1))) u32x4*)(out + ((row0 + r) * N + col) * 2) = v[i];
+        if (r < rows && col < cols)
+            *(__attribute__((address_space(1))) u32x4*)(out + ((row0 + r) * ld + col) * 2) = v[i];
     }
 }
 
@@ -497,6 +515,7 @@ template <int PASS, int MB, int NB>
 __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const LinTile& t, int mw, int cw, uint8_t* stage,
                                                   const float* bias, int lane, f32x16 (&acc)[MB][NB]) {
     static_assert(NB == 2, "64 columns a wave");
+    static_assert(PASS != kLinDh8, "store_tile_dh8");
     // (the addresses below depend on the lane alone: computed before the tile
     // loop and kept, they took more registers than there are)
     asm volatile("" : "+v"(lane));
@@ -512,7 +531,7 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
                 for (int p = 0; p < 2; ++p)
                     store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
             }
-            stage_out(stage, a.out, t.row0, t.rows, a.N, mw + 32 * mb, cw, lane);
+            stage_out(stage, a.out, t.row0, t.rows, a.N, a.N, mw + 32 * mb, cw, lane);
         }
     } else {
         // this lane's columns: cw + 32 nb + 16 p + 8 half .. +7; z of one block
@@ -560,7 +579,7 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
                     for (int p = 0; p < 2; ++p)
                         store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
                 }
-                stage_out(stage, a.zsave, t.row0, t.rows, a.N, m, cw, lane);
+                stage_out(stage, a.zsave, t.row0, t.rows, a.N, a.N, m, cw, lane);
             }
             if (a.codes != nullptr) {
                 // 64 codes a row, 16 bytes at position chunk ^ (row / 2) % 4
@@ -618,7 +637,108 @@ __device__ __forceinline__ void store_tile_staged(const LinearArgs& a, const Lin
                     store16(stage_at(stage, lr, 4 * nb + 2 * p + half), ActVec<bf16_t>::pack(v[p]));
                 }
             }
-            stage_out(stage, a.out, t.row0, t.rows, a.N, m, cw, lane);
+            stage_out(stage, a.out, t.row0, t.rows, a.N, a.N, m, cw, lane);
+        }
+    }
+}
+
+// a staged 32 x 32 block (64 bytes a row, 16-byte chunk c at c ^ (row / 2) % 4)
+// out to rows m .. (below `rows`, counted from row0), columns c .. of a bf16
+// array with ld values a row
+__device__ __forceinline__ uint8_t* stage32_at(uint8_t* stage, int row, int chunk) {
+    return stage + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void stage32_out(uint8_t* stage, uint8_t* out, int64_t row0, int rows, int ld, int m, int c,
+                                            int lane) {
+    u32x4 v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = load16(stage32_at(stage, 16 * i + (lane >> 2), lane & 3));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = m + 16 * i + (lane >> 2);
+        if (r < rows)
+            *(__attribute__((address_space(1))) u32x4*)(out + ((row0 + r) * ld + c + 8 * (lane & 3)) * 2) = v[i];
+    }
+}
+
+// dhid of a wave's WM x 64 block -> da = dhid b s (1 + a (1 - s)) (s =
+// sigmoid(a)), db = dhid silu(a) and hid = silu(a) b, from a and b in 8 bits.
+// The codes of 32 rows x 64 columns come in 16 bytes a lane (row lane / 4 +
+// 16 i, chunk lane % 4), through the staging area to the lanes that hold those
+// columns; the next rows' are loaded before the last of this one's stores. The
+// outputs go out 32 columns at a time, hid and da side by side in the staging
+// area, then db: 64 columns of all three took more registers than there are.
+// N % 64 == 0: a wave's columns all exist.
+template <int MB, int NB>
+__device__ __forceinline__ void store_tile_dh8(const LinearArgs& a, const LinTile& t, int mw, int cw, uint8_t* stage,
+                                               int lane, f32x16 (&acc)[MB][NB]) {
+    asm volatile("" : "+v"(lane));  // (as above)
+    const int lr = lane & 31, half = lane >> 5;
+    const int col = (a.same_rows ? t.g * a.N : 0) + cw;
+    const int c2 = (a.same_rows ? 2 * t.g * a.N : 0) + cw;
+    u32x4 cd[2][2];
+    uint32_t sc[NB][2];
+    auto load_codes = [&](int mb) {
+        const int m = mw + 32 * mb, last = t.rows - 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t at = (t.row0 + min(m + 16 * i + (lane >> 2), last)) * a.ldp + col + 16 * (lane & 3);
+            cd[0][i] = *(const __attribute__((address_space(1))) u32x4*)(a.ca + at);
+            cd[1][i] = *(const __attribute__((address_space(1))) u32x4*)(a.cb + at);
+        }
+        const int64_t blk = ((t.row0 + min(m + lr, last)) * a.ldp + col) / kRows8Block;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            sc[nb][0] = *(const __attribute__((address_space(1))) uint8_t*)(a.sa + blk + nb);
+            sc[nb][1] = *(const __attribute__((address_space(1))) uint8_t*)(a.sb + blk + nb);
+        }
+    };
+    load_codes(0);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        const int m = mw + 32 * mb;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) store16(stage_at(stage, 16 * i + (lane >> 2), 4 * q + (lane & 3)), cd[q][i]);
+        uint2 w[NB][2][2];  // this lane's codes: [block][a, b][run]
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    w[nb][q][p] = *reinterpret_cast<const uint2*>(stage_at(stage, lr, 4 * q + 2 * nb + p) + 8 * half);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            __builtin_amdgcn_sched_barrier(0);
+            const float sa = rows8_step(sc[nb][0]), sb = rows8_step(sc[nb][1]);
+            float dh[2][8];
+            block_runs(acc[mb][nb], dh);
+            u32x4 vb[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float da[8], db[8], hd[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float av = rows8_value(u < 4 ? w[nb][0][p].x : w[nb][0][p].y, u & 3, sa);
+                    const float bv = rows8_value(u < 4 ? w[nb][1][p].x : w[nb][1][p].y, u & 3, sb);
+                    const float sg = lin_sigmoid(av), sil = av * sg;
+                    da[u] = dh[p][u] * bv * (sg * __builtin_fmaf(av, 1.0f - sg, 1.0f));
+                    db[u] = dh[p][u] * sil;
+                    hd[u] = sil * bv;
+                }
+                store16(stage32_at(stage, lr, 2 * p + half), ActVec<bf16_t>::pack(hd));
+                store16(stage32_at(stage + 2048, lr, 2 * p + half), ActVec<bf16_t>::pack(da));
+                vb[p] = ActVec<bf16_t>::pack(db);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (nb + 1 == NB && mb + 1 < MB) load_codes(mb + 1);
+            stage32_out(stage, a.hid, t.row0, t.rows, a.ldp, m, col + 32 * nb, lane);
+            stage32_out(stage + 2048, a.out, t.row0, t.rows, 2 * a.ldp, m, c2 + 32 * nb, lane);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) store16(stage32_at(stage, lr, 2 * p + half), vb[p]);
+            stage32_out(stage, a.out, t.row0, t.rows, 2 * a.ldp, m, c2 + a.N + 32 * nb, lane);
         }
     }
 }

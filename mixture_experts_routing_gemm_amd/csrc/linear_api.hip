@@ -28,6 +28,7 @@ hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream
 int64_t linear_db_tiles(int64_t R, int G);
 hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st);
 hipError_t launch_linear_db(const DbArgs& a, bool f32, hipStream_t st);
+hipError_t launch_linear_pair(int pass, const LinearArgs& r, const LinearArgs& s, int shape, hipStream_t st);
 hipError_t launch_linear_backward(const LinearArgs& x, const LinearArgs& w, const DbArgs& d, bool f32, hipStream_t st);
 hipError_t launch_pack_rows8(int64_t rows, int n, bool f32, const void* x, void* packed, hipStream_t st);
 hipError_t launch_unpack_rows8(int64_t rows, int n, bool f32, const void* packed, void* x, hipStream_t st);
@@ -46,7 +47,8 @@ int32_t check_linear(const moe_linear_shape* s, bool grouped) {
     if (s->act != MOE_F32 && s->act != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     if (s->grad != MOE_F32 && s->grad != s->act) return MOE_ERR_UNSUPPORTED;
     const int unit = s->act == MOE_F32 ? 4 : 8;
-    if (s->rows >= (int64_t(1) << 31) || s->n_in > (1 << 20) || s->n_out > (1 << 20) || s->n_in % unit != 0 ||
+    // (row counts are rounded up to tiles and parts in 32 bits)
+    if (s->rows > (int64_t(1) << 31) - 4096 || s->n_in > (1 << 20) || s->n_out > (1 << 20) || s->n_in % unit != 0 ||
         s->n_out % unit != 0 || s->groups > kMaxGroups)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
@@ -89,7 +91,8 @@ constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f, 1.0f}, {k
 // the units, the last one in between, and for parts the join: about 7 us, and
 // its float32 sums written and read at 4 TB/s. The rows of a group are not
 // known here: half a tile of each group is taken to be empty.
-Plan plan_of(const moe_linear_shape& s, int pass) {
+// smallest: the last tile shape to consider, with k whole (0: any, and parts)
+Plan plan_of(const moe_linear_shape& s, int pass, int smallest = 0) {
     const bool f32 = s.act == MOE_F32;
     const TileCost* const first = f32 ? kF32Tiles : kBf16Tiles;
     const TileCost* const last = first + (f32 ? 2 : pass == kLinDw ? 3 : 4);
@@ -102,11 +105,11 @@ Plan plan_of(const moe_linear_shape& s, int pass) {
     const float extras = pass != kLinForward ? 0.0f
                                              : static_cast<float>((s.fn != MOE_FN_NONE) + (s.save != MOE_SAVE_NONE));
     Plan best{first->shape, 1, -1.0f};
-    for (const TileCost* c = first; c != last; ++c) {
+    for (const TileCost* c = first; c != last && (smallest == 0 || c->shape <= smallest); ++c) {
         const int64_t mt = pass == kLinDw ? groups * ((s.n_out + c->bm - 1) / c->bm)
                                           : s.groups == 1 ? (s.rows + c->bm - 1) / c->bm : s.rows / c->bm + (groups + 1) / 2;
         const int64_t tiles = mt * ((n + c->bn - 1) / c->bn);
-        for (int parts = 1; parts <= 16 && parts * 4 <= slices + 3; ++parts) {
+        for (int parts = 1; parts <= (smallest == 0 ? 16 : 1) && parts * 4 <= slices + 3; ++parts) {
             if (parts > 1 && tiles * parts > 4 * units) break;
             const int64_t all = tiles * parts, rounds = all / units;
             const float rest = static_cast<float>(all - rounds * units) / units;
@@ -128,6 +131,14 @@ bool few_rows(const moe_linear_shape& s) {
     const int64_t groups = std::min<int64_t>(s.groups, s.rows);
     return s.rows <= s.groups * int64_t(s.groups == 1 ? 32 : 8) &&
            groups * ((s.n_out + 127) / 128) < device_cus();
+}
+
+// The tile shape of the SwiGLU experts' backward products over the routed rows
+// (n columns, k values), which take whole k and stage their outputs: the
+// three largest shapes.
+int pair_shape(const moe_shape& s, int n, int k) {
+    const moe_linear_shape l{s.T * s.k, n, k, s.E, MOE_BF16, MOE_FN_NONE, MOE_SAVE_NONE, MOE_BF16};
+    return plan_of(l, kLinDx, kLinTileMid).shape;
 }
 
 // dx, dW and db in one launch, on 128 x 128 (float32: 64 x 64) tiles, k not
@@ -330,6 +341,84 @@ int32_t check_rows8(int64_t rows, int32_t n, int32_t dtype, const void* x, const
 }
 
 }  // namespace
+
+namespace moe {
+
+// dhid = dy W2 and the SwiGLU backward of every routed row and shared-expert
+// block, from a and b in 8 bits (saved8): [da | db] rows and hid rows
+hipError_t launch_ffn_dh8(const moe_shape& s, const int32_t* offsets, const void* w2, const void* dy_perm,
+                          const void* dy_sh, const void* saved8, void* h_r, void* h_s, void* dd_r, void* dd_s,
+                          hipStream_t st) {
+    const Saved8Layout L = saved8_layout(s);
+    const uint8_t* sv = static_cast<const uint8_t*>(saved8);
+    const int64_t wgroup = static_cast<int64_t>(s.d) * s.h * 2;
+    LinearArgs r{}, q{};
+    r.a = static_cast<const uint8_t*>(dy_perm);
+    r.b = static_cast<const uint8_t*>(w2);
+    r.offsets = offsets;
+    r.R = s.T * s.k;
+    r.G = s.E;
+    r.N = s.h;
+    r.K = s.d;
+    r.parts = 1;
+    r.out = static_cast<uint8_t*>(dd_r);
+    r.ca = sv + L.a_r;
+    r.cb = sv + L.b_r;
+    r.sa = r.ca + L.scales_r;
+    r.sb = r.cb + L.scales_r;
+    r.hid = static_cast<uint8_t*>(h_r);
+    r.ldp = s.h;
+    if (s.S > 0) {
+        q = r;
+        q.a = static_cast<const uint8_t*>(dy_sh);
+        q.b = r.b + s.E * wgroup;
+        q.offsets = nullptr;
+        q.same_rows = 1;
+        q.R = s.T;
+        q.G = s.S;
+        q.out = static_cast<uint8_t*>(dd_s);
+        q.ca = sv + L.a_s;
+        q.cb = sv + L.b_s;
+        q.sa = q.ca + L.scales_s;
+        q.sb = q.cb + L.scales_s;
+        q.hid = static_cast<uint8_t*>(h_s);
+        q.ldp = s.S * s.h;
+    }
+    return launch_linear_pair(kLinDh8, r, q, pair_shape(s, s.h, s.d), st);
+}
+
+// dv = [da | db] [W1; W3] of every routed row; the shared experts' blocks side
+// by side along k, so that their sum is the product's own
+hipError_t launch_ffn_dx2(const moe_shape& s, const int32_t* offsets, const void* w1, const void* w3, const void* dd_r,
+                          const void* dd_s, void* dx_perm, void* dx_sh, hipStream_t st) {
+    const int64_t wgroup = static_cast<int64_t>(s.d) * s.h * 2;
+    LinearArgs r{}, q{};
+    r.a = static_cast<const uint8_t*>(dd_r);
+    r.b = static_cast<const uint8_t*>(w1);
+    r.b2 = static_cast<const uint8_t*>(w3);
+    r.seg = s.h;
+    r.offsets = offsets;
+    r.R = s.T * s.k;
+    r.G = s.E;
+    r.N = s.d;
+    r.K = 2 * s.h;
+    r.parts = 1;
+    r.out = static_cast<uint8_t*>(dx_perm);
+    if (s.S > 0) {
+        q = r;
+        q.a = static_cast<const uint8_t*>(dd_s);
+        q.b = r.b + s.E * wgroup;
+        q.b2 = r.b2 + s.E * wgroup;
+        q.offsets = nullptr;
+        q.R = s.T;
+        q.G = 1;
+        q.K = 2 * s.S * s.h;
+        q.out = static_cast<uint8_t*>(dx_sh);
+    }
+    return launch_linear_pair(kLinDx2, r, q, pair_shape(s, s.d, 2 * s.h), st);
+}
+
+}  // namespace moe
 
 extern "C" {
 

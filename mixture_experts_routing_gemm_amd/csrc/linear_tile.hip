@@ -237,6 +237,12 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
         const uint8_t* b;
         int valid_a, valid_b, k, kend, list;
         int first, g, c0;  // forward: this is the tile's first slice; its group and column
+        int kb, seg;       // kLinDx2: k within the segment of b; the segment's number
+    };
+    // kLinDx2: the first row of segment i of the tile's k, at the tile's column
+    auto segment = [&](int g, int i, int c0) {
+        const uint8_t* w = (i & 1) != 0 ? a.b2 : a.b;
+        return w + (static_cast<int64_t>(g + (i >> 1)) * a.seg * a.N + c0) * ES;
     };
     auto next_source = [&](int list) {
         Source src;
@@ -266,10 +272,11 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                 src.b = a.b + (wbase + t.c0 * ldb) * ES;
                 src.valid_b = min(BN, a.N - t.c0);
             } else {
-                src.b = a.b + (wbase + t.c0) * ES;
+                src.b = PASS == kLinDx2 ? segment(t.g, 0, t.c0) : a.b + (wbase + t.c0) * ES;
                 src.valid_b = a.N - t.c0;
             }
         }
+        src.kb = src.seg = 0;
         return src;
     };
     Source src;
@@ -278,7 +285,8 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
     bool in_a, in_b;  // this lane's chunk lies before the end of k
     auto open_slice = [&](int slot) {
         rsa = OpA::resource(src.a, lda, src.k, src.kend, src.valid_a);
-        rsb = OpB::resource(src.b, ldb, src.k, src.kend, src.valid_b);
+        rsb = PASS == kLinDx2 ? OpB::resource(src.b, ldb, src.kb, src.kend > src.k ? a.seg : 0, src.valid_b)
+                              : OpB::resource(src.b, ldb, src.k, src.kend, src.valid_b);
         in_a = PASS == kLinDw || kc < src.kend - src.k;
         in_b = PASS != kLinForward || kc < src.kend - src.k;
         slot_addr = __builtin_amdgcn_readfirstlane(lin_lds_addr(lds) + slot * kSlot);
@@ -305,6 +313,14 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
     };
     auto close_slice = [&]() {
         src.k += SK;
+        if constexpr (PASS == kLinDx2) {  // (seg is a multiple of SK)
+            src.kb += SK;
+            if (src.kb >= a.seg && src.k < src.kend) {
+                src.kb = 0;
+                ++src.seg;
+                src.b = segment(src.g, src.seg, src.c0);
+            }
+        }
         if (src.k >= src.kend) src = next_source(src.list);
     };
     // slot numbers go round
@@ -370,13 +386,16 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
     }
     wait_vmcnt<(SLOTS - 2) * REQS>();
     ring_barrier();
-    static_for<0, MB + NB>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        if constexpr (i < NB)
-            fb0[i] = frag_b(0, ic<0>(), i);
-        else
-            fa0[i - NB] = frag_a(0, ic<0>(), i - NB);
-    });
+    auto first_fragments = [&](uint32_t slot_off) {
+        static_for<0, MB + NB>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            if constexpr (i < NB)
+                fb0[i] = frag_b(slot_off, ic<0>(), i);
+            else
+                fa0[i - NB] = frag_a(slot_off, ic<0>(), i - NB);
+        });
+    };
+    first_fragments(0);
 
     int slot = 0;   // of the next slice to compute
     int relax = 0;  // steps left whose wait may leave the last tile's stores under way
@@ -433,12 +452,17 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                 // the slot before is free until the next step's requests
                 if (!idle) {
                     uint8_t* stage = lds + slot_after(slot, SLOTS - 1) * kSlot + wave * 4096;
-                    store_tile_staged<PASS, MB, NB>(a, t, mw, cw, stage, bias_lds[it & 3], lane, acc);
+                    if constexpr (PASS == kLinDh8)
+                        store_tile_dh8<MB, NB>(a, t, mw, cw, stage, lane, acc);
+                    else
+                        store_tile_staged<PASS, MB, NB>(a, t, mw, cw, stage, bias_lds[it & 3], lane, acc);
                 }
                 relax = !idle && mw + S::WM <= t.rows && cw + S::WN <= a.N ? SLOTS - 2 : 0;
                 ring_barrier();  // every wave is done with its stage
+                // (read again, so that they take no registers in the epilogue)
+                first_fragments(slot * kSlot);
             }
-        } else if (!idle) {
+        } else if (PASS <= kLinDw && !idle) {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -459,6 +483,18 @@ __global__ __launch_bounds__(lin_threads<S>())
     __attribute__((amdgpu_waves_per_eu(lin_waves_per_simd<S>(), lin_waves_per_simd<S>())))
 void linear_tile_kernel(LinearArgs a) {
     linear_tiles<T, PASS, S>(a, blockIdx.x, gridDim.x);
+}
+
+// Two sets of tiles in one launch, `first` of the work-groups on the first (a
+// multiple of 8): the routed experts' and the shared ones'.
+template <typename T, int PASS, class S>
+__global__ __launch_bounds__(lin_threads<S>())
+    __attribute__((amdgpu_waves_per_eu(lin_waves_per_simd<S>(), lin_waves_per_simd<S>())))
+void linear_pair_kernel(LinearArgs r, LinearArgs s, int first) {
+    if (static_cast<int>(blockIdx.x) < first)
+        linear_tiles<T, PASS, S>(r, blockIdx.x, first);
+    else
+        linear_tiles<T, PASS, S>(s, blockIdx.x - first, gridDim.x - first);
 }
 
 // dx, dW and db of a small layer in one launch: none needs another's result,
@@ -486,7 +522,8 @@ template <int PASS, class S>
 unsigned tile_grid(LinearArgs& a) {
     a.ntn = (a.N + S::BN - 1) / S::BN;
     a.mtiles = PASS == kLinDw ? (a.M + S::BM - 1) / S::BM : 0;
-    const int64_t mt = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.mtiles : a.R / S::BM + a.G;
+    const int64_t mt = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.mtiles
+                                      : a.same_rows ? a.G * ((a.R + S::BM - 1) / S::BM) : a.R / S::BM + a.G;
     const int64_t tiles = mt * a.ntn * a.parts;
     if (tiles >= (int64_t(1) << 30)) return 0;
     const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(device_cus()) * S::PER_CU, tiles);
@@ -521,6 +558,39 @@ hipError_t launch_backward(const LinearArgs& x0, const LinearArgs& w0, const DbA
     return hipGetLastError();
 }
 
+template <int PASS, class S>
+hipError_t launch_pair(const LinearArgs& r0, const LinearArgs& s0, hipStream_t st) {
+    constexpr int ring = S::SLOTS * lin_slot<S>();
+    static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_pair_kernel<bf16_t, PASS, S>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (attr != hipSuccess) return attr;
+    LinearArgs r = r0, s = s0;
+    unsigned nr = tile_grid<PASS, S>(r), ns = s.out != nullptr ? tile_grid<PASS, S>(s) : 0;
+    if (nr == 0 || (s.out != nullptr && ns == 0)) return hipErrorInvalidValue;
+    // where there are not units enough for both, they are shared out by work
+    // (each set with a work-group for every unit, the second set's tiles began
+    // when the first's were done: dx of 4096 tokens, eight experts of 32 and two
+    // shared, whose tiles take twice as long, 558 us)
+    const unsigned units = static_cast<unsigned>(device_cus() * S::PER_CU) & ~7u;
+    if (ns > 0 && nr + ns > units) {
+        const double wr = static_cast<double>(r.R) * r.K, ws = static_cast<double>(s.R) * s.K * (s.same_rows ? s.G : 1);
+        const unsigned part = (static_cast<unsigned>(units * (ws / (wr + ws))) + 7) & ~7u;
+        ns = std::min(ns, std::max(8u, std::min(part, units - 8)));
+        nr = std::min(nr, units - ns);
+    }
+    linear_pair_kernel<bf16_t, PASS, S><<<nr + ns, lin_threads<S>(), ring, st>>>(r, s, static_cast<int>(nr));
+    return hipGetLastError();
+}
+
+template <int PASS>
+hipError_t launch_pair_shape(const LinearArgs& r, const LinearArgs& s, int shape, hipStream_t st) {
+    switch (shape) {
+        case kLinTileBig: return launch_pair<PASS, LinBig>(r, s, st);
+        case kLinTileHalf: return launch_pair<PASS, LinHalf>(r, s, st);
+        default: return launch_pair<PASS, LinMid>(r, s, st);
+    }
+}
+
 template <int PASS>
 hipError_t launch_pass(const LinearArgs& a, int shape, bool f32, hipStream_t st) {
     if (f32) return shape == kLinTileMid ? launch<float, PASS, LinMid>(a, st) : launch<float, PASS, LinTiny>(a, st);
@@ -536,6 +606,12 @@ hipError_t launch_pass(const LinearArgs& a, int shape, bool f32, hipStream_t st)
 }
 
 }  // namespace
+
+// kLinDh8 or kLinDx2, the routed experts' tiles and (s.out not NULL) the shared
+// experts'; bf16, Big, Half or Mid
+hipError_t launch_linear_pair(int pass, const LinearArgs& r, const LinearArgs& s, int shape, hipStream_t st) {
+    return pass == kLinDh8 ? launch_pair_shape<kLinDh8>(r, s, shape, st) : launch_pair_shape<kLinDx2>(r, s, shape, st);
+}
 
 // dx, dW and db together (out or db NULL: not computed), 128 x 128 tiles in
 // bf16, 64 x 64 in float32, k not split

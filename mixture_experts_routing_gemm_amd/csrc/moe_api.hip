@@ -29,7 +29,7 @@ hipError_t launch_grouped_ffn(const moe_shape& s, const void* x_perm, const floa
                               hipStream_t st, const Marks* mk, const int32_t* gather = nullptr,
                               void* pre_a_r = nullptr, void* pre_b_r = nullptr, void* pre_a_s = nullptr,
                               void* pre_b_s = nullptr, void* saved8 = nullptr);
-bool ffn_backward_big(const moe_shape& s);
+bool ffn_saved8_supported(const moe_shape& s);
 bool use_big_tiles(const moe_shape& s);
 // whether the whole-layer forward's up-projection reads its routed rows from
 // x through src_token (bf16 rows, persistent tiles) instead of from x_perm
@@ -64,10 +64,16 @@ hipError_t launch_grouped_ffn_f8w(const moe_shape& s, const void* x_perm, const 
 hipError_t launch_ffn_backward(const moe_shape& s, const void* x_perm, const float* qparams,
                                const int32_t* offsets, const void* x, const void* w1,
                                const void* w3, const void* w2, const void* dy_perm,
-                               const void* dy_sh, void* dx_perm, void* dx_sh, void* dw1,
-                               void* dw3, void* dw2, void* ws, hipStream_t st,
-                               const Marks* mk, const void* saved = nullptr,
-                               const void* saved8 = nullptr, bool dw_bf16 = false);
+                               const void* dy_sh, void* dx_perm, void* dx_sh, float* dw1,
+                               float* dw3, float* dw2, void* ws, hipStream_t st,
+                               const Marks* mk, const void* saved = nullptr);
+size_t ffn_backward8_ws_bytes(const moe_shape& s);
+hipError_t launch_ffn_backward8(const moe_shape& s, const void* x_perm, const float* qparams,
+                                const int32_t* offsets, const void* x, const void* w1,
+                                const void* w3, const void* w2, const void* saved8,
+                                const void* dy_perm, const void* dy_sh, void* dx_perm, void* dx_sh,
+                                void* dw1, void* dw3, void* dw2, bool dw_bf16, void* ws,
+                                hipStream_t st);
 
 __global__ void clear_header_kernel(uint32_t* hdr) { hdr[threadIdx.x] = 0u; }
 
@@ -101,7 +107,7 @@ size_t act_bytes(int32_t dt) { return dt == MOE_F32 ? 4 : (dt == MOE_BF16 ? 2 : 
 
 struct Layout {
     size_t x8 = 0, q8 = 0, h8_r = 0, h8_s = 0, hsc_r = 0, hsc_s = 0;  // fp8-weight forward
-    size_t fbwd = 0, part = 0, rank = 0, blk = 0, pre = 0, loads = 0, qstats = 0, plan = 0, x_perm = 0, qparams = 0, h_r = 0, h_s = 0, y_perm = 0,
+    size_t fbwd = 0, fbwd8 = 0, part = 0, rank = 0, blk = 0, pre = 0, loads = 0, qstats = 0, plan = 0, x_perm = 0, qparams = 0, h_r = 0, h_s = 0, y_perm = 0,
            y_sh = 0, total = 0;
 };
 
@@ -159,7 +165,12 @@ Layout layout(const moe_shape& s, int stage) {
         // plan, recomputed a / b / hidden rows and their gradients
         L.fbwd = take(ffn_backward_ws_bytes(s));
     }
-    L.total = (disp || ffn || stage == MOE_STAGE_GATE_BACKWARD || stage == MOE_STAGE_FFN_BACKWARD)
+    if (stage == MOE_STAGE_FFN_BACKWARD8) {
+        // hidden rows and the gradients of a and b
+        L.fbwd8 = take(ffn_backward8_ws_bytes(s));
+    }
+    L.total = (disp || ffn || stage == MOE_STAGE_GATE_BACKWARD || stage == MOE_STAGE_FFN_BACKWARD ||
+               stage == MOE_STAGE_FFN_BACKWARD8)
                   ? off
                   : 0;
     return L;
@@ -315,7 +326,8 @@ const char* const kKernelNames[] = {"gate_topk",  "dispatch_rank", "dispatch_sca
 extern "C" {
 
 size_t moe_workspace_bytes(const moe_shape* s, int32_t stage) {
-    if (stage < MOE_STAGE_GATE || stage > MOE_STAGE_FORWARD_FP8W) return 0;
+    if ((stage < MOE_STAGE_GATE || stage > MOE_STAGE_FORWARD_FP8W) && stage != MOE_STAGE_FFN_BACKWARD8) return 0;
+    if (stage == MOE_STAGE_FFN_BACKWARD8 && moe_ffn_saved8_bytes(s) == 0) return 0;
     if (stage == MOE_STAGE_FORWARD_FP8W && (check_shape(s, true) != MOE_OK || !f8w_shape_ok(*s)))
         return 0;
     const bool ffn = stage == MOE_STAGE_FFN || stage == MOE_STAGE_FORWARD;
@@ -554,7 +566,7 @@ int32_t moe_grouped_ffn_backward_saved(const moe_shape* s, const void* x_perm,
 }
 
 size_t moe_ffn_saved8_bytes(const moe_shape* s) {
-    if (check_shape(s, true) != MOE_OK || s->act != MOE_BF16 || !ffn_backward_big(*s)) return 0;
+    if (check_shape(s, true) != MOE_OK || s->act != MOE_BF16 || !ffn_saved8_supported(*s)) return 0;
     return saved8_layout(*s).bytes;
 }
 
@@ -564,7 +576,7 @@ int32_t moe_grouped_ffn_save8(const moe_shape* s, const void* x_perm, const floa
                               void* saved8, size_t saved8_bytes, void* ws, size_t ws_bytes,
                               void* stream) {
     MOE_TRY(check_shape(s, true));
-    if (s->act != MOE_BF16 || !ffn_backward_big(*s)) return MOE_ERR_UNSUPPORTED;
+    if (s->act != MOE_BF16 || !ffn_saved8_supported(*s)) return MOE_ERR_UNSUPPORTED;
     if (s->T == 0) return MOE_OK;
     MOE_TRY(check_ptrs({x_perm, offsets, w1, w3, w2, y_perm, saved8}));
     if (s->S > 0) MOE_TRY(check_ptrs({x, y_shared}));
@@ -589,7 +601,7 @@ int32_t moe_grouped_ffn_backward_saved8(const moe_shape* s, const void* x_perm,
                                         void* dx_shared, int32_t grad, void* dw1, void* dw3,
                                         void* dw2, void* ws, size_t ws_bytes, void* stream) {
     MOE_TRY(check_shape(s, true));
-    if (s->act != MOE_BF16 || !ffn_backward_big(*s)) return MOE_ERR_UNSUPPORTED;
+    if (s->act != MOE_BF16 || !ffn_saved8_supported(*s)) return MOE_ERR_UNSUPPORTED;
     if (grad != MOE_F32 && grad != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     MOE_TRY(check_ptrs({w1, w3, w2, dw1, dw3, dw2}));
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -610,12 +622,11 @@ int32_t moe_grouped_ffn_backward_saved8(const moe_shape* s, const void* x_perm,
     else if (dx_shared != nullptr || dy_shared != nullptr) return MOE_ERR_INVALID_ARG;
     if (s->dispatch == MOE_FP8_E4M3) MOE_TRY(check_ptrs({qparams}));
     MOE_TRY(check_opt({x, qparams}));
-    MOE_TRY(check_ws(*s, MOE_STAGE_FFN_BACKWARD, ws, ws_bytes));
-    const Layout L = layout(*s, MOE_STAGE_FFN_BACKWARD);
-    return hip_status(launch_ffn_backward(*s, x_perm, qparams, offsets, x, w1, w3, w2, dy_perm,
-                                          dy_shared, dx_perm, dx_shared, dw1, dw3, dw2,
-                                          at<void>(ws, L.fbwd), st, nullptr, nullptr, saved8,
-                                          grad == MOE_BF16));
+    MOE_TRY(check_ws(*s, MOE_STAGE_FFN_BACKWARD8, ws, ws_bytes));
+    const Layout L = layout(*s, MOE_STAGE_FFN_BACKWARD8);
+    return hip_status(launch_ffn_backward8(*s, x_perm, qparams, offsets, x, w1, w3, w2, saved8,
+                                           dy_perm, dy_shared, dx_perm, dx_shared, dw1, dw3, dw2,
+                                           grad == MOE_BF16, at<void>(ws, L.fbwd8), st));
 }
 
 size_t moe_fp8_weight_scale_floats(const moe_shape* s) {

@@ -49,7 +49,7 @@ class Case:
         f = lambda r, dt=torch.bfloat16: torch.full((r, d), 77.0, dtype=dt, device="cuda")  # noqa: E731
         self.y, self.dx = f(T * k), f(T * k)
         self.ys, self.dxs = (f(T), f(T)) if S else (None, None)
-        self.ws, self.bws = mm.alloc_workspace(self.shape, mm.STAGE_FFN), mm.alloc_workspace(self.shape, mm.STAGE_FFN_BACKWARD)
+        self.ws, self.bws = mm.alloc_workspace(self.shape, mm.STAGE_FFN), mm.alloc_workspace(self.shape, mm.STAGE_FFN_BACKWARD8)
 
     def forward(self, which="save8"):
         mm, v = _mm(), self.dev
@@ -158,3 +158,52 @@ def test_saved8_forward_and_backward(case):
         again = c.backward(grad)
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(dw, again))
+
+
+def test_no_tokens_zeroes_the_weight_gradients():
+    mm = _mm()
+    s = mm.make_shape(0, 256, 4, 2, 1, 128, "bf16")
+    for grad, t in (("f32", torch.float32), ("bf16", torch.bfloat16)):
+        dw = [torch.full((5, 128, 256), 7.0, dtype=t, device="cuda") for _ in range(2)]
+        dw.append(torch.full((5, 256, 128), 7.0, dtype=t, device="cuda"))
+        w = [torch.ones_like(v, dtype=torch.bfloat16) for v in dw]
+        mm.moe_grouped_ffn_save8(s, None, None, None, None, *w, None, None, None, None)
+        mm.moe_grouped_ffn_backward_saved8(s, None, None, None, None, *w, None, None, None, None, None, grad, *dw, None)
+        torch.cuda.synchronize()
+        assert not any(v.any() for v in dw)
+
+
+def test_saved8_captured_and_replayed():
+    """Forward and backward in one graph, replayed on other inputs with eager
+    calls between: every replay has the eager result's bits."""
+    c, other = Case(260, 512, 4, 2, 1, 256, "skewed", seed=3), Case(130, 512, 4, 2, 1, 256, "even", seed=4)
+    mm, v = _mm(), c.dev
+    dw = [torch.empty_like(v[n]) for n in ("w1", "w3", "w2")]
+
+    def step():
+        c.forward()
+        mm.moe_grouped_ffn_backward_saved8(c.shape, v["x_perm"], None, c.offd, v["x"], v["w1"], v["w3"], v["w2"], c.saved, v["dy"],
+                                           v["dys"], c.dx, c.dxs, "bf16", *dw, c.bws)
+    outs = [c.y, c.ys, c.dx, c.dxs, *dw]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            step()
+    torch.cuda.synchronize()
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    for i in range(4):
+        for n in ("x", "x_perm", "dy", "dys"):
+            v[n].copy_(torch.randn(v[n].shape, device="cuda", generator=gen))
+        step()
+        torch.cuda.synchronize()
+        ref = [t.clone() for t in outs]
+        for t in outs:
+            t.fill_(3.0)
+        other.forward()
+        other.backward("f32")
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref)), f"replay {i}"
