@@ -91,15 +91,16 @@ def make_offsets(rows, groups, kind, seed=0):
 
 
 class Layer:
-    """Inputs of one layer on the CPU, and what float64 says of it."""
+    """Inputs of one layer, on the CPU or (large ones) the GPU, and what float64 says of it."""
 
-    def __init__(self, rows, n_in, n_out, offsets, kind="bf16", fn="none", bias=True, residual=False, seed=0):
-        g = torch.Generator().manual_seed(seed)
+    def __init__(self, rows, n_in, n_out, offsets, kind="bf16", fn="none", bias=True, residual=False, seed=0,
+                 device="cpu"):
+        g = torch.Generator(device=device).manual_seed(seed)
         G = len(offsets) - 1
         t = TYPES[kind]
 
         def rnd(*s, sigma=1.0):
-            return (torch.randn(*s, generator=g) * sigma)
+            return (torch.randn(*s, generator=g, device=device) * sigma)
         self.rows, self.n_in, self.n_out, self.offsets, self.kind, self.fn = rows, n_in, n_out, offsets, kind, fn
         self.x = rnd(rows, n_in).to(t)
         self.w = rnd(G, n_out, n_in, sigma=n_in ** -0.5).to(t)
@@ -115,7 +116,7 @@ class Layer:
 
     def forward(self):
         """y, z and the bounds of their errors; None rows stay NaN."""
-        nan = lambda: torch.full((self.rows, self.n_out), float("nan"), dtype=torch.float64)  # noqa: E731
+        nan = lambda: torch.full((self.rows, self.n_out), float("nan"), dtype=torch.float64, device=self.x.device)  # noqa: E731
         y, z, ey, ez = nan(), nan(), nan(), nan()
         for g, lo, hi in self.groups():
             x, w = self.x[lo:hi].double(), self.w[g].double()
@@ -137,10 +138,12 @@ class Layer:
     def backward(self, zs, grad):
         """dx, dw, db and their bounds, from the saved pre-activations zs."""
         G = len(self.offsets) - 1
-        dx = torch.full((self.rows, self.n_in), float("nan"), dtype=torch.float64)
+        f64 = dict(dtype=torch.float64, device=self.x.device)
+        dx = torch.full((self.rows, self.n_in), float("nan"), **f64)
         ex = dx.clone()
-        dw, ew = torch.zeros(G, self.n_out, self.n_in).double(), torch.zeros(G, self.n_out, self.n_in).double()
-        db, eb = torch.zeros(G, self.n_out).double(), torch.zeros(G, self.n_out).double()
+        dw, ew = torch.zeros(G, self.n_out, self.n_in, **f64), torch.zeros(G, self.n_out, self.n_in, **f64)
+        db, eb = torch.zeros(G, self.n_out, **f64), torch.zeros(G, self.n_out, **f64)
+        zs = None if zs is None else zs.to(self.x.device)
         half_in = HALF[self.kind] if self.fn != "none" else 0.0  # dz is rounded to the act type
         for g, lo, hi in self.groups():
             x, w, dy = self.x[lo:hi].double(), self.w[g].double(), self.dy[lo:hi].double()
@@ -165,7 +168,8 @@ class Layer:
 
 def within(got, ref, bound, what):
     """got within the bound of ref, element by element, where ref is a number."""
-    got, there = got.double().cpu(), ~torch.isnan(ref)
+    got, ref, bound = got.double().cpu(), ref.cpu(), bound.cpu()
+    there = ~torch.isnan(ref)
     assert torch.isfinite(got[there]).all(), f"{what}: not finite"
     over = (got[there] - ref[there]).abs() - bound[there]
     if over.numel():

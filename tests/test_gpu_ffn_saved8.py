@@ -96,6 +96,7 @@ CASES = [
     (77, 512, 3, 2, 2, 384, "holes", False),
     (300, 256, 8, 4, 0, 640, "last", False),
     (200, 256, 4, 2, 1, 256, "skewed", True),
+    (4000, 512, 4, 2, 2, 640, "skewed", False),  # the larger tiles
 ]
 
 

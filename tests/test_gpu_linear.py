@@ -73,7 +73,8 @@ class Run:
     def check_forward(self):
         y, z, ey, ez = self.L.forward()
         within(self.y, y, ey, "y")
-        none = torch.isnan(y[:, 0])  # rows of no group keep what they held
+        z, ez = z.cpu(), ez.cpu()
+        none = torch.isnan(y[:, 0]).cpu()  # rows of no group keep what they held
         assert bool((self.y.cpu()[none] == 77.0).all())
         if self.save == "act":
             within(self.saved_z(), z, ez + HALF[self.L.kind] * (z.abs() + ez), "z")
@@ -87,7 +88,7 @@ class Run:
         zs = self.saved_z() if self.save != "none" else None
         dx, dw, db, ex, ew, eb = self.L.backward(zs, self.grad)
         within(self.dx, dx, ex, "dx")
-        none = torch.isnan(dx[:, 0])
+        none = torch.isnan(dx[:, 0]).cpu()
         assert bool((self.dx.cpu()[none] == 77.0).all())
         within(self.dw, dw, ew, "dw")
         within(self.db, db, eb, "db")
@@ -129,6 +130,38 @@ def test_grouped_forward_and_backward(case, kind):
     torch.cuda.synchronize()
     r.check_backward()
     assert _mm().moe_get_device_error(r.ws) == 0 and _mm().moe_get_device_error(r.bws) == 0
+
+
+# large enough for each tile shape and for k in parts, with edges in every
+# direction (float64 on the GPU)
+LARGE = [
+    ("bf16", 8000, 2056, 4000, 1, "even", "int8"),     # 256 x 256 forward and dW
+    ("bf16", 9000, 200, 1544, 6, "skewed", "act"),     # 256 x 128
+    ("bf16", 6000, 1032, 2056, 5, "gap", "int8"),
+    ("bf16", 33000, 72, 264, 9, "skewed", "int8"),     # 128 x 128, dW in parts
+    ("bf16", 100, 4104, 2056, 1, "even", "act"),       # few rows, long k in parts
+    ("bf16", 3000, 4104, 104, 40, "holes", "act"),
+    ("f32", 3000, 516, 1028, 3, "skewed", "act"),
+    ("f32", 20000, 100, 68, 1, "even", "int8"),        # dW in parts
+    ("f32", 40, 4100, 2052, 2, "even", "act"),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "-".join(map(str, c)))
+def test_large_layers(case):
+    kind, rows, n_in, n_out, G, how, save = case
+    L = Layer(rows, n_in, n_out, make_offsets(rows, G, how, 5), kind, "silu", residual=True, seed=rows, device="cuda")
+    r = Run(L, save=save)
+    r.forward()
+    r.backward()
+    torch.cuda.synchronize()
+    r.check_forward()
+    r.check_backward()
+    first = [t.clone() for t in (r.y, r.dx, r.dw, r.db)]
+    r.forward()
+    r.backward()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((r.y, r.dx, r.dw, r.db), first))  # the same bits
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
