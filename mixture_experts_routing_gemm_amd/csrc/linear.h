@@ -749,8 +749,22 @@ __device__ __forceinline__ void store_tile_dh8(const LinearArgs& a, const LinTil
 // at once and they load and compute in step; 512 x 128: 8 against 15.)
 constexpr int kDzRows = 32;
 
+struct DzArgs {
+    const int32_t* offsets;
+    int64_t R;
+    int G, N, fn;
+    const uint8_t* dy;       // [R, N] (act)
+    const uint8_t* z;        // [R, N] (act) or NULL
+    const uint8_t* codes;    // [R, n32] or NULL
+    const uint8_t* scales;
+    int64_t n32;
+    uint8_t* dz;             // [R, N] (act) or NULL
+    float* db_part;          // [blocks of 32 rows of a group][N] or NULL
+};
+
 struct DbArgs {
     const int32_t* offsets;
+    uint32_t* hdr;       // error flag of the workspace
     int64_t R;
     int G, N;
     const float* part;   // [blocks of kDzRows rows of a group][N], or NULL:
@@ -766,7 +780,7 @@ template <typename T, int SPLIT>
 __device__ __forceinline__ void linear_db_block(const DbArgs& a, int g, int cb) {
     __shared__ GroupWalk walk;
     __shared__ float sums[SPLIT][64];
-    walk_groups(walk, a.offsets, a.R, a.G, kDzRows, nullptr);
+    walk_groups(walk, a.offsets, a.R, a.G, kDzRows, g == 0 && cb == 0 ? a.hdr : nullptr);
     const int c = threadIdx.x & 63, col = cb * 64 + c, q = threadIdx.x >> 6;
     float s = 0.0f;
     if (col < a.N) {

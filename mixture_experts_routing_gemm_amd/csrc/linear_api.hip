@@ -8,19 +8,6 @@
 
 namespace moe {
 
-struct DzArgs {
-    const int32_t* offsets;
-    int64_t R;
-    int G, N, fn;
-    const uint8_t* dy;
-    const uint8_t* z;
-    const uint8_t* codes;
-    const uint8_t* scales;
-    int64_t n32;
-    uint8_t* dz;
-    float* db_part;
-};
-
 int device_cus();
 hipError_t launch_linear_tile(int pass, const LinearArgs& a, int shape, bool f32, hipStream_t st);
 hipError_t launch_linear_rows(const LinearArgs& a, int fb, bool f32, hipStream_t st);
@@ -316,6 +303,7 @@ int32_t linear_backward(const moe_linear_shape* s, const void* x, const int32_t*
     }
     DbArgs b_args{};
     b_args.offsets = off;
+    b_args.hdr = static_cast<uint32_t*>(ws);
     b_args.R = s->rows;
     b_args.G = s->groups;
     b_args.N = s->n_out;

@@ -2,24 +2,13 @@
 // gradient's partial sums, those sums joined, and the sums of a product that
 // was split along k joined (with the forward's epilogue, or as dx or dW).
 // All are bound by HBM.
+#include <algorithm>
+
 #include "linear.h"
 
 namespace moe {
 
 constexpr int kDzCols = 256;
-
-struct DzArgs {
-    const int32_t* offsets;
-    int64_t R;
-    int G, N, fn;
-    const uint8_t* dy;       // [R, N] (act)
-    const uint8_t* z;        // [R, N] (act) or NULL
-    const uint8_t* codes;    // [R, n32] or NULL
-    const uint8_t* scales;
-    int64_t n32;
-    uint8_t* dz;             // [R, N] (act) or NULL
-    float* db_part;          // [blocks of 32 rows of a group][N] or NULL
-};
 
 // A work-group takes 32 rows of one group and 256 columns: eight rows of 32
 // lanes x 8 columns at a time. dz is rounded to the act type once (the
@@ -31,54 +20,56 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(DzArgs a) {
     __shared__ GroupWalk walk;
     __shared__ float sums[8][kDzCols];
     walk_groups(walk, a.offsets, a.R, a.G, kDzRows, nullptr);
-    const int mt = blockIdx.x;
-    if (mt >= walk.pre[a.G]) return;
-    const int g = group_of(walk, a.G, mt);
-    const int m0 = (mt - walk.pre[g]) * kDzRows;
-    const int rows = min(kDzRows, walk.off[g + 1] - walk.off[g] - m0);
-    const int64_t row0 = walk.off[g] + m0;
     const int cl = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
     const int c = blockIdx.y * kDzCols + cl;
     const int nv = min(8, max(0, a.N - c));
-    float s[8];
+    // (more than one round only past the largest grid)
+    for (int mt = blockIdx.x; mt < walk.pre[a.G]; mt += gridDim.x) {
+        const int g = group_of(walk, a.G, mt);
+        const int m0 = (mt - walk.pre[g]) * kDzRows;
+        const int rows = min(kDzRows, walk.off[g + 1] - walk.off[g] - m0);
+        const int64_t row0 = walk.off[g] + m0;
+        float s[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s[u] = 0.0f;
-    if (nv > 0) {
+        for (int u = 0; u < 8; ++u) s[u] = 0.0f;
+        if (nv > 0) {
 #pragma unroll 4
-        for (int r = rl; r < rows; r += 8) {
-            const int64_t row = row0 + r;
-            float v[8], z[8];
-            load8<T>(a.dy, row * a.N + c, nv, v);
-            if (a.fn != MOE_FN_NONE) {
-                if (a.z != nullptr) {
-                    load8<T>(a.z, row * a.N + c, nv, z);
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + row * a.n32 + c);
-                    const float step = rows8_step(a.scales[row * (a.n32 / kRows8Block) + c / kRows8Block]);
+            for (int r = rl; r < rows; r += 8) {
+                const int64_t row = row0 + r;
+                float v[8], z[8];
+                load8<T>(a.dy, row * a.N + c, nv, v);
+                if (a.fn != MOE_FN_NONE) {
+                    if (a.z != nullptr) {
+                        load8<T>(a.z, row * a.N + c, nv, z);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(a.codes + row * a.n32 + c);
+                        const float step = rows8_step(a.scales[row * (a.n32 / kRows8Block) + c / kRows8Block]);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        z[u] = rows8_value(w.x, u, step);
-                        z[4 + u] = rows8_value(w.y, u, step);
+                        for (int u = 0; u < 4; ++u) {
+                            z[u] = rows8_value(w.x, u, step);
+                            z[4 + u] = rows8_value(w.y, u, step);
+                        }
                     }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] *= lin_slope(a.fn, z[u]);
+                    store8<T>(a.dz, row * a.N + c, nv, v);
                 }
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] *= lin_slope(a.fn, z[u]);
-                store8<T>(a.dz, row * a.N + c, nv, v);
+                for (int u = 0; u < 8; ++u) s[u] += v[u];
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) s[u] += v[u];
         }
-    }
-    if (a.db_part == nullptr) return;
+        if (a.db_part == nullptr) continue;
+        __syncthreads();  // (the round before is done with the sums)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) sums[rl][cl + u] = s[u];
-    __syncthreads();
-    const int col = blockIdx.y * kDzCols + threadIdx.x;
-    if (col < a.N) {
-        float t = 0.0f;
+        for (int u = 0; u < 8; ++u) sums[rl][cl + u] = s[u];
+        __syncthreads();
+        const int col = blockIdx.y * kDzCols + threadIdx.x;
+        if (col < a.N) {
+            float t = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) t += sums[r][threadIdx.x];
-        a.db_part[static_cast<int64_t>(mt) * a.N + col] = t;
+            for (int r = 0; r < 8; ++r) t += sums[r][threadIdx.x];
+            a.db_part[static_cast<int64_t>(mt) * a.N + col] = t;
+        }
     }
 }
 
@@ -142,8 +133,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
 int64_t linear_db_tiles(int64_t R, int G) { return R / kDzRows + G; }
 
 hipError_t launch_linear_dz(const DzArgs& a, bool f32, hipStream_t st) {
-    const int64_t mt = linear_db_tiles(a.R, a.G);
-    if (mt >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    // (a grid has at most 2^32 - 1 threads along x)
+    const int64_t mt = std::min<int64_t>(linear_db_tiles(a.R, a.G), (int64_t(1) << 24) - 1);
     const dim3 grid(static_cast<unsigned>(mt), (a.N + kDzCols - 1) / kDzCols);
     if (f32)
         linear_dz_kernel<float><<<grid, 256, 0, st>>>(a);

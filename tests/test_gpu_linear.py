@@ -412,6 +412,41 @@ def test_operands_past_4_gib():
     within(dw[1], ref, (last + 2) * 2.0 ** -24 * (d.abs().T @ a.abs()), "dw")
 
 
+@pytest.mark.parametrize("wanted", ["dx", "dw", "db"])
+@pytest.mark.parametrize("rows,fn", [(40, "none"), (40, "silu"), (2500, "none")])
+def test_bad_offsets_are_reported_by_each_gradient_alone(rows, fn, wanted):
+    mm = _mm()
+    bad = np.array([0, rows // 2, rows // 3, rows], dtype=np.int32)
+    L = Layer(rows, 72, 136, np.array([0, rows // 2, rows // 2, rows], dtype=np.int32), "bf16", fn, seed=4)
+    r = Run(L, save="none" if fn == "none" else "act")
+    r.forward()
+    r.off = torch.from_numpy(bad).cuda()
+    o = [getattr(r, n) if n == wanted else None for n in ("dx", "dw", "db")]
+    mm.moe_grouped_linear_backward(r.s, r.x, r.off, r.w, r.saved, r.dy, *o, r.bws)
+    assert mm.moe_get_device_error(r.bws) == mm.MOE_ERR_BAD_INDEX
+
+
+def test_more_rows_than_one_grid_of_the_bias_gradient():
+    """2^29 + 96 rows: more blocks of 32 rows than a launch has work-groups of
+    256 threads. dy is 1 in a few rows and 0 elsewhere, so the sums are exact."""
+    mm = _mm()
+    rows, n = 2 ** 29 + 96, 8
+    s = mm.make_linear_shape(rows, n, n, fn="relu", save="act", grad="f32")
+    saved = mm.alloc_linear_saved(s)
+    z = saved[:rows * n * 2].view(torch.bfloat16).view(rows, n)
+    z.fill_(1.0)
+    dy = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 31, 32, rows // 2, 2 ** 29 - 33, 2 ** 29 - 32, 2 ** 29, rows - 1], device="cuda")
+    for c in range(n):
+        dy[at[:c + 1], c] = 1.0
+    z[at[-1], 7] = -1.0
+    db = torch.full((1, n), 9.0, device="cuda")
+    ws = mm.alloc_linear_workspace(s, mm.STAGE_LINEAR_BACKWARD)
+    mm.moe_linear_backward(s, None, None, saved, dy, None, None, db, ws)
+    torch.cuda.synchronize()
+    assert db[0].tolist() == [1.0, 2.0, 3.0, 4.0, 5.0, 6.0, 7.0, 7.0]
+
+
 def _rel(a, b):
     return float((a.double() - b.double()).norm() / b.double().norm())
 
