@@ -26,8 +26,15 @@ constexpr int kMaxGroups = 256;
 // kLinDx2 is dx of the up-projections, [da | db] [W1; W3], k running over
 // segments of W1 and W3 in turn.
 enum LinearPass { kLinForward = 0, kLinDx = 1, kLinDw = 2, kLinDh8 = 3, kLinDx2 = 4 };
-// output tiles: 256 x 256, 256 x 128, 128 x 128, 64 x 128, 64 x 64
-enum LinTileShape { kLinTileBig = 0, kLinTileHalf = 1, kLinTileMid = 2, kLinTileSmall = 3, kLinTileTiny = 4 };
+// output tiles: 256 x 256, 256 x 128, 128 x 128, 64 x 128, 64 x 64, 64 x 32
+enum LinTileShape {
+    kLinTileBig = 0,
+    kLinTileHalf = 1,
+    kLinTileMid = 2,
+    kLinTileSmall = 3,
+    kLinTileTiny = 4,
+    kLinTileSlim = 5
+};
 
 struct LinearArgs {
     const uint8_t* a;        // x (forward), dz (dx, dW)

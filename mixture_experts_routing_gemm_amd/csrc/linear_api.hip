@@ -60,10 +60,11 @@ struct Plan {
 // for a tile that has a unit to itself in a round that is not full. Measured
 // at 4096 values of k on an MI355X (forward, dx and dW alike):
 // bf16 256 x 256 tiles reach 1.13 PFLOP/s, 256 x 128 0.94, 128 x 128 0.82 and
-// 64 x 128 0.63, float32 128 x 128 132 TFLOP/s and 64 x 64 121; smaller tiles
-// win where the larger ones leave units idle.
-// `epilogue`: what an activation and saved pre-activations each add to a tile (two work-groups on a unit hide half of it in each other's
-// products).
+// 64 x 128 0.63, float32 128 x 128 132 TFLOP/s, 64 x 64 119 and 64 x 32 109;
+// smaller tiles win where the larger ones leave units idle (512 x 512 values
+// of 4096 products in float32: 64 x 64 tiles 77 us, 64 x 32 51).
+// `epilogue`: what an activation and saved pre-activations each add to a tile
+// (two work-groups on a unit hide half of it in each other's products).
 struct TileCost {
     int shape, bm, bn;
     float full, one, epilogue;
@@ -72,17 +73,20 @@ constexpr TileCost kBf16Tiles[] = {{kLinTileBig, 256, 256, 0.96f, 0.64f, 8.0f},
                                    {kLinTileHalf, 256, 128, 0.57f, 0.52f, 3.0f},
                                    {kLinTileMid, 128, 128, 0.345f, 0.33f, 1.5f},
                                    {kLinTileSmall, 64, 128, 0.215f, 0.24f, 0.8f}};
-constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f, 1.0f}, {kLinTileTiny, 64, 64, 0.276f, 0.4f, 0.5f}};
+constexpr TileCost kF32Tiles[] = {{kLinTileMid, 128, 128, 1.01f, 1.0f, 1.0f},
+                                  {kLinTileTiny, 64, 64, 0.283f, 0.29f, 0.5f},
+                                  {kLinTileSlim, 64, 32, 0.157f, 0.19f, 0.3f}};
 
 // The cheapest tile shape and number of parts by those costs: whole rounds of
 // the units, the last one in between, and for parts the join: about 7 us, and
-// its float32 sums written and read at 4 TB/s. The rows of a group are not
+// its float32 sums written and read at 4 TB/s (dW of 128 x 128 weights over
+// 30000 rows: 45 us in 8 parts, 29 in 16, 24 in 32 and in 64). The rows of a group are not
 // known here: half a tile of each group is taken to be empty.
 // smallest: the last tile shape to consider, with k whole (0: any, and parts)
 Plan plan_of(const moe_linear_shape& s, int pass, int smallest = 0) {
     const bool f32 = s.act == MOE_F32;
     const TileCost* const first = f32 ? kF32Tiles : kBf16Tiles;
-    const TileCost* const last = first + (f32 ? 2 : pass == kLinDw ? 3 : 4);
+    const TileCost* const last = first + (f32 || pass == kLinDw ? 3 : 4);
     const int64_t units = device_cus(), sk = f32 ? 16 : 32;
     const int64_t n = pass == kLinForward ? s.n_out : s.n_in;
     const int64_t groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
@@ -96,11 +100,14 @@ Plan plan_of(const moe_linear_shape& s, int pass, int smallest = 0) {
         const int64_t mt = pass == kLinDw ? groups * ((s.n_out + c->bm - 1) / c->bm)
                                           : s.groups == 1 ? (s.rows + c->bm - 1) / c->bm : s.rows / c->bm + (groups + 1) / 2;
         const int64_t tiles = mt * ((n + c->bn - 1) / c->bn);
-        for (int parts = 1; parts <= (smallest == 0 ? 16 : 1) && parts * 4 <= slices + 3; ++parts) {
+        // 1, 2, 3, 4, 6, 8, 12 .. 64 parts
+        for (int parts = 1; parts <= (smallest == 0 ? 64 : 1) && parts * 4 <= slices + 3;
+             parts = parts < 4 ? parts + 1 : (parts & (parts - 1)) == 0 ? parts + parts / 2 : parts / 3 * 4) {
             if (parts > 1 && tiles * parts > 4 * units) break;
             const int64_t all = tiles * parts, rounds = all / units;
             const float rest = static_cast<float>(all - rounds * units) / units;
-            const float round = rounds * c->full + (rest > 0.0f ? c->one + (c->full - c->one) * rest : 0.0f);
+            const float round =
+                std::max(c->one, rounds * c->full + (rest > 0.0f ? c->one + (c->full - c->one) * rest : 0.0f));
             float us = static_cast<float>((slices + parts - 1) / parts) * round;
             us += extras * c->epilogue * (parts > 1 ? 0 : rounds + (rest > 0.0f ? 1 : 0));
             if (parts > 1) us += 7.0f + values * parts * (8.0f / 4e6f);
@@ -128,14 +135,16 @@ int pair_shape(const moe_shape& s, int n, int k) {
     return plan_of(l, kLinDx, kLinTileMid).shape;
 }
 
-// dx, dW and db in one launch, on 128 x 128 (float32: 64 x 64) tiles, k not
+// dx, dW and db in one launch, on 128 x 128 (float32: 64 x 32) tiles, k not
 // split: where the longer of the two products, or both together spread over
 // the units, take less than one after the other by their own plans and the 6
-// us that a launch takes to begin and end (512 x 64 -> 128 in float32: 12 us
-// against 27, 300 x 512 -> 512 in bf16 17 against 31).
+// us that a launch takes to begin and end. Replayed from a graph: 512 rows of
+// 64 -> 128, eight groups, in float32 6 us against 14 apart; in bf16 300 rows
+// of 512 -> 512 11 against 22, 2048 rows of 1024 -> 2048 36 against 60; 8000
+// rows of 256 -> 256, whose dW needs its parts, 83 against 37.
 bool backward_together(const moe_linear_shape& s, const Plan& dx, const Plan& dw) {
     const bool f32 = s.act == MOE_F32;
-    const TileCost& c = f32 ? kF32Tiles[1] : kBf16Tiles[2];
+    const TileCost& c = f32 ? kF32Tiles[2] : kBf16Tiles[2];
     const int64_t sk = f32 ? 16 : 32, groups = std::min<int64_t>(s.groups, std::max<int64_t>(1, s.rows));
     const int64_t nt = (s.n_in + c.bn - 1) / c.bn;
     const float sx = static_cast<float>((s.n_out + sk - 1) / sk), sw = static_cast<float>((s.rows / groups + sk - 1) / sk);

@@ -78,17 +78,21 @@ __global__ __launch_bounds__(512) void linear_db_kernel(DbArgs a) {
     linear_db_block<T, 8>(a, blockIdx.y, blockIdx.x);
 }
 
-// The parts' sums of 32 x 32 values a wave, added part by part, then stored as
-// the tile kernels store a block.
-template <typename T, int PASS>
+// The parts' sums of 32 x 32 values, added part by part, then stored as the
+// tile kernels store a block. A block is one wave's (SPLIT = 1), or four waves
+// (SPLIT = 4) sum every fourth part each, in order, and then their sums in
+// order: where many parts are added over few blocks, which are then as long as
+// the loads that one wave has under way.
+template <typename T, int PASS, int SPLIT>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
     __shared__ GroupWalk walk;
+    __shared__ float sums[SPLIT > 1 ? SPLIT - 1 : 1][16][64];
     if constexpr (PASS != kLinDw) walk_groups(walk, a.offsets, a.R, a.G, 1, nullptr);
-    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5;
     const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
     const int nblk = (a.N + 31) / 32;
-    const int64_t blk = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (blk >= (all + 31) / 32 * nblk) return;
+    const int64_t blk = SPLIT > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 4 + wave;
+    if (blk >= (all + 31) / 32 * nblk) return;  // (SPLIT > 1: never)
     const int c0 = static_cast<int>(blk % nblk) * 32;
     const int64_t row = blk / nblk * 32 + (lane & 31);
     bool ok = row < all;
@@ -113,13 +117,26 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
         for (int u = 0; u < 8; ++u) v[p][u] = 0.0f;
         const int c = c0 + 16 * p + 8 * half, nv = min(8, a.N - c);
         if (ok && nv > 0) {
-            for (int s = 0; s < a.parts; ++s) {
+#pragma unroll 4
+            for (int s = SPLIT > 1 ? wave : 0; s < a.parts; s += SPLIT) {
                 float t[8];
                 load8<float>(reinterpret_cast<const uint8_t*>(a.part_out), (s * all + row) * a.N + c, nv, t);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v[p][u] += t[u];
             }
         }
+    }
+    if constexpr (SPLIT > 1) {
+        if (wave > 0) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) sums[wave - 1][u][lane] = v[u >> 3][u & 7];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int w = 0; w < SPLIT - 1; ++w)
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v[u >> 3][u & 7] += sums[w][u][lane];
     }
     if constexpr (PASS == kLinForward) {
         linear_epilogue32<T>(a, g, row, c0, half, ok, v, a.N);
@@ -152,22 +169,26 @@ hipError_t launch_linear_db(const DbArgs& a, bool f32, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st) {
-    const int64_t all = pass == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
-    const int64_t blocks = ((all + 31) / 32 * ((a.N + 31) / 32) + 3) / 4;
-    if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    const unsigned n = static_cast<unsigned>(blocks);
-    if (pass == kLinForward) {
-        if (f32) linear_join_kernel<float, kLinForward><<<n, 256, 0, st>>>(a);
-        else linear_join_kernel<bf16_t, kLinForward><<<n, 256, 0, st>>>(a);
-    } else if (pass == kLinDx) {
-        if (f32) linear_join_kernel<float, kLinDx><<<n, 256, 0, st>>>(a);
-        else linear_join_kernel<bf16_t, kLinDx><<<n, 256, 0, st>>>(a);
-    } else {
-        if (f32) linear_join_kernel<float, kLinDw><<<n, 256, 0, st>>>(a);
-        else linear_join_kernel<bf16_t, kLinDw><<<n, 256, 0, st>>>(a);
-    }
+namespace {
+template <typename T, int PASS>
+hipError_t launch_join(const LinearArgs& a, hipStream_t st) {
+    const int64_t all = PASS == kLinDw ? static_cast<int64_t>(a.G) * a.M : a.R;
+    const int64_t blocks = (all + 31) / 32 * ((a.N + 31) / 32);
+    if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+    if (a.parts >= 8)
+        linear_join_kernel<T, PASS, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
+    else
+        linear_join_kernel<T, PASS, 1><<<static_cast<unsigned>((blocks + 3) / 4), 256, 0, st>>>(a);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_linear_join(int pass, const LinearArgs& a, bool f32, hipStream_t st) {
+    switch (pass) {
+        case kLinForward: return f32 ? launch_join<float, kLinForward>(a, st) : launch_join<bf16_t, kLinForward>(a, st);
+        case kLinDx: return f32 ? launch_join<float, kLinDx>(a, st) : launch_join<bf16_t, kLinDx>(a, st);
+        default: return f32 ? launch_join<float, kLinDw>(a, st) : launch_join<bf16_t, kLinDw>(a, st);
+    }
 }
 
 }  // namespace moe

@@ -36,10 +36,12 @@ __device__ __forceinline__ int lin_swz(int r) { return ((r >> 1) & 3) ^ ((r >> 3
 __device__ __forceinline__ int lin_koff(int r, int c) { return (r << 6) + ((c ^ lin_swz(r)) << 4); }
 // chunk swizzle of slice row k of an m- or n-contiguous operand. bf16: the
 // transposing reads (4 rows of 32 or 64 bytes at a time) hit distinct banks;
-// float32: so do the two halves of a wave, which read rows four apart.
-template <typename T>
+// float32: so do the two halves of a wave, which read rows four apart (rows of
+// W >= 64 values; the 32 of a narrower one have the same banks in each row).
+template <typename T, int W>
 __device__ __forceinline__ int lin_tsw(int k) {
-    return sizeof(T) == 2 ? (0xEA40 >> (4 * (k & 3))) & 15 : ((k >> 2) & 1) << 3;  // bf16: 0, 4, 10, 14
+    if constexpr (sizeof(T) == 2) return (0xEA40 >> (4 * (k & 3))) & 15;  // 0, 4, 10, 14
+    else return W >= 64 ? ((k >> 2) & 1) << 3 : 0;
 }
 
 __device__ __forceinline__ uint32_t lin_lds_addr(const uint8_t* p) {
@@ -67,33 +69,50 @@ __device__ __forceinline__ i32x4lin lin_rsrc(const uint8_t* base, uint32_t bytes
 }
 
 // The tile shapes: BM x BN by waves of WM x WN, SLOTS slots of the ring, the
-// first ISS waves issue the requests, PER_CU work-groups a compute unit.
+// first ISS waves issue the requests, PER_CU work-groups a compute unit; KG
+// sets of such waves, each with a ring of its own and its share of the tile's
+// k, whose sums are added in the end. A step of one set is a chain (barrier,
+// LDS reads, products) that takes three times as long as its products: a
+// second set on the unit takes its steps meanwhile, where there is no second
+// tile to do so.
 struct LinBig {
-    static constexpr int BM = 256, BN = 256, WM = 128, WN = 64, ISS = 8, SLOTS = 4, PER_CU = 1;
+    static constexpr int BM = 256, BN = 256, WM = 128, WN = 64, ISS = 8, SLOTS = 4, PER_CU = 1, KG = 1;
 };
 struct LinHalf {
-    static constexpr int BM = 256, BN = 128, WM = 128, WN = 64, ISS = 4, SLOTS = 3, PER_CU = 2;
+    static constexpr int BM = 256, BN = 128, WM = 128, WN = 64, ISS = 4, SLOTS = 3, PER_CU = 2, KG = 1;
 };
 struct LinMid {
-    static constexpr int BM = 128, BN = 128, WM = 64, WN = 64, ISS = 4, SLOTS = 4, PER_CU = 2;
+    static constexpr int BM = 128, BN = 128, WM = 64, WN = 64, ISS = 4, SLOTS = 4, PER_CU = 2, KG = 1;
 };
 struct LinSmall {
-    static constexpr int BM = 64, BN = 128, WM = 32, WN = 64, ISS = 4, SLOTS = 4, PER_CU = 3;
+    static constexpr int BM = 64, BN = 128, WM = 32, WN = 64, ISS = 4, SLOTS = 4, PER_CU = 3, KG = 1;
 };
 struct LinTiny {
-    static constexpr int BM = 64, BN = 64, WM = 32, WN = 32, ISS = 4, SLOTS = 4, PER_CU = 4;
+    static constexpr int BM = 64, BN = 64, WM = 32, WN = 32, ISS = 4, SLOTS = 4, PER_CU = 2, KG = 2;
 };
+struct LinSlim {
+    static constexpr int BM = 64, BN = 32, WM = 32, WN = 32, ISS = 2, SLOTS = 4, PER_CU = 3, KG = 2;
+};
+// waves of a set, threads of a work-group
+template <class S>
+constexpr int lin_waves() {
+    return (S::BM / S::WM) * (S::BN / S::WN);
+}
 template <class S>
 constexpr int lin_threads() {
-    return (S::BM / S::WM) * (S::BN / S::WN) * 64;
+    return lin_waves<S>() * S::KG * 64;
 }
 template <class S>
 constexpr int lin_slot() {
     return (S::BM + S::BN) * 64;
 }
 template <class S>
+constexpr int lin_ring() {
+    return S::KG * S::SLOTS * lin_slot<S>();
+}
+template <class S>
 constexpr int lin_waves_per_simd() {
-    return lin_threads<S>() / 256 * S::PER_CU;
+    return lin_threads<S>() * S::PER_CU / 256;
 }
 
 // One operand's side of the request stream. TR: contiguous along m or n
@@ -109,7 +128,7 @@ struct LinOperand {
         if constexpr (TR) {
             constexpr int CH = W * ES / 16;  // 16-byte chunks a row
             const int k = i * (64 / CH) + lane / CH;
-            return static_cast<uint32_t>(k * ld * ES) + 16u * ((lane % CH) ^ lin_tsw<T>(k));
+            return static_cast<uint32_t>(k * ld * ES) + 16u * ((lane % CH) ^ lin_tsw<T, W>(k));
         } else {
             const int r = 16 * i + (lane >> 2);
             return static_cast<uint32_t>(r * ld * ES) + 16u * ((lane & 3) ^ lin_swz(r));
@@ -138,10 +157,10 @@ struct LinOperand {
             const int g = lane >> 4, s = lane & 15;
             const int k = 16 * ks + 8 * (g >> 1) + (s >> 2);
             const int f = f0 + 16 * (g & 1) + 4 * (s & 3);
-            return static_cast<uint32_t>(k * W * 2 + (((f >> 3) ^ lin_tsw<T>(k)) << 4) + (f & 7) * 2);
+            return static_cast<uint32_t>(k * W * 2 + (((f >> 3) ^ lin_tsw<T, W>(k)) << 4) + (f & 7) * 2);
         } else {
             const int k = 8 * ks + 4 * (lane >> 5), f = f0 + (lane & 31);
-            return static_cast<uint32_t>(k * W * 4 + (((f >> 2) ^ lin_tsw<T>(k)) << 4) + (f & 3) * 4);
+            return static_cast<uint32_t>(k * W * 4 + (((f >> 2) ^ lin_tsw<T, W>(k)) << 4) + (f & 3) * 4);
         }
     }
     // 16 bytes of k values of one feature: bf16 k = 16 ks + 8 (lane / 32) ..
@@ -201,18 +220,26 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
     // so that a store instruction writes 8 rows x 128 bytes: as the
     // accumulators hold them (32 rows x 32 bytes) a 256 x 256 tile's stores
     // took 29 thousand cycles, as long as 23 slices of k.
-    constexpr bool kStage = ES == 2 && S::WN == 64 && kSlot >= lin_threads<S>() / 64 * 4096;
+    constexpr int KG = S::KG, WAVES = lin_waves<S>();
+    constexpr bool kStage = ES == 2 && S::WN == 64 && (KG > 1 || kSlot >= WAVES * 4096);
+    // the other sets' sums (KG > 1), and the staging area behind them
+    constexpr int kSums = (KG - 1) * WAVES * MB * NB * 4096;
+    static_assert(KG == 1 || kSums + (kStage ? WAVES * 4096 : 0) <= lin_ring<S>(), "LDS of the epilogue");
+    static_assert(KG == 1 || PASS <= kLinDw, "one segment");
     // stores of a full tile by a wave, at least (see the waits below)
-    constexpr int kStores = kStage ? 4 * MB : 0;
+    constexpr int kStores = kStage && KG == 1 ? 4 * MB : 0;
 
     walk_groups(walk, a.offsets, a.R, a.G, BM, bid == 0 ? a.hdr : nullptr);
     if constexpr (PASS == kLinDw) order_groups(order, walk, a.G);
 
     const int tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    // the set, its ring, and the wave within it
+    const int set = KG > 1 ? wave_all / WAVES : 0, wave = KG > 1 ? wave_all % WAVES : wave_all;
+    const int ring = set * SLOTS * kSlot;
     const int wm = wave / WN_WAVES, wn = wave % WN_WAVES;
     const int lr = lane & 31, lg = lane >> 5;
-    const bool issuer = S::ISS * 64 == lin_threads<S>() || wave < S::ISS;
+    const bool issuer = S::ISS == WAVES || wave < S::ISS;
 
     // row strides in values
     const int64_t lda = PASS == kLinDw ? a.M : a.K;
@@ -244,15 +271,8 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
         const uint8_t* w = (i & 1) != 0 ? a.b2 : a.b;
         return w + (static_cast<int64_t>(g + (i >> 1)) * a.seg * a.N + c0) * ES;
     };
-    auto next_source = [&](int list) {
+    auto source_of = [&](const LinTile& t, bool more, int list) {
         Source src;
-        LinTile t;
-        bool more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
-        ++list;
-        while (more && t.k1 <= t.k0) {  // (a group without rows, or an empty part)
-            more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
-            ++list;
-        }
         src.list = list;
         src.first = more ? 1 : 0;
         src.g = t.g;
@@ -279,6 +299,16 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
         src.kb = src.seg = 0;
         return src;
     };
+    auto next_source = [&](int list) {
+        LinTile t;
+        bool more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
+        ++list;
+        while (more && t.k1 <= t.k0) {  // (a group without rows, or an empty part)
+            more = lin_tile<PASS, BM, BN, SK>(a, walk, order, bid, nblk, list, t);
+            ++list;
+        }
+        return source_of(t, more, list);
+    };
     Source src;
     i32x4lin rsa, rsb;
     uint32_t slot_addr;
@@ -289,10 +319,10 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                               : OpB::resource(src.b, ldb, src.k, src.kend, src.valid_b);
         in_a = PASS == kLinDw || kc < src.kend - src.k;
         in_b = PASS != kLinForward || kc < src.kend - src.k;
-        slot_addr = __builtin_amdgcn_readfirstlane(lin_lds_addr(lds) + slot * kSlot);
+        slot_addr = __builtin_amdgcn_readfirstlane(lin_lds_addr(lds) + ring + slot * kSlot);
         if constexpr (PASS == kLinForward && kStage) {
             // the tile's bias (zeros without one) lands before its first slice
-            if (wave == 0 && src.first != 0) {
+            if (wave_all == 0 && src.first != 0) {
                 const uint32_t bytes = a.bias != nullptr ? min(BN, a.N - src.c0) * 4 : 0;
                 lin_dma16(lin_rsrc(reinterpret_cast<const uint8_t*>(a.bias + static_cast<int64_t>(src.g) * a.N + src.c0), bytes),
                           16u * lane,
@@ -321,7 +351,8 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                 src.b = segment(src.g, src.seg, src.c0);
             }
         }
-        if (src.k >= src.kend) src = next_source(src.list);
+        // (several sets: past its share a set requests zeros)
+        if (KG == 1 && src.k >= src.kend) src = next_source(src.list);
     };
     // slot numbers go round
     auto slot_after = [](int s, int n) { return s + n >= SLOTS ? s + n - SLOTS : s + n; };
@@ -342,16 +373,16 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
     auto frag_a = [&](uint32_t slot_off, auto KS, int i) -> u32x4 {
         constexpr int ks = decltype(KS)::value;
         if constexpr (PASS == kLinDw)
-            return OpA::fragment(lds, slot_off + fo_a[i] + ks * 32 * BM);
+            return OpA::fragment(lds, ring + slot_off + fo_a[i] + ks * 32 * BM);
         else
-            return OpA::fragment(lds, slot_off + fo_a[ks] + i * 2048);
+            return OpA::fragment(lds, ring + slot_off + fo_a[ks] + i * 2048);
     };
     auto frag_b = [&](uint32_t slot_off, auto KS, int i) -> u32x4 {
         constexpr int ks = decltype(KS)::value;
         if constexpr (PASS != kLinForward)
-            return OpB::fragment(lds, slot_off + fo_b[i] + ks * 32 * BN);
+            return OpB::fragment(lds, ring + slot_off + fo_b[i] + ks * 32 * BN);
         else
-            return OpB::fragment(lds, slot_off + fo_b[ks] + i * 2048);
+            return OpB::fragment(lds, ring + slot_off + fo_b[ks] + i * 2048);
     };
 
     f32x16 acc[MB][NB];
@@ -377,15 +408,6 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
         });
     };
 
-    // prologue: all slots but one
-    src = next_source(0);
-    for (int s = 0; s < SLOTS - 1; ++s) {
-        open_slice(s);
-        if (issuer) static_for<0, REQS>(request);
-        close_slice();
-    }
-    wait_vmcnt<(SLOTS - 2) * REQS>();
-    ring_barrier();
     auto first_fragments = [&](uint32_t slot_off) {
         static_for<0, MB + NB>([&](auto I) {
             constexpr int i = decltype(I)::value;
@@ -395,7 +417,21 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                 fa0[i - NB] = frag_a(slot_off, ic<0>(), i - NB);
         });
     };
-    first_fragments(0);
+    // all slots but one
+    auto fill_ring = [&]() {
+        for (int s = 0; s < SLOTS - 1; ++s) {
+            open_slice(s);
+            if (issuer) static_for<0, REQS>(request);
+            close_slice();
+        }
+        wait_vmcnt<(SLOTS - 2) * REQS>();
+        ring_barrier();
+        first_fragments(0);
+    };
+    if constexpr (KG == 1) {
+        src = next_source(0);
+        fill_ring();
+    }
 
     int slot = 0;   // of the next slice to compute
     int relax = 0;  // steps left whose wait may leave the last tile's stores under way
@@ -408,7 +444,17 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
             for (int j = 0; j < NB; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        const int KT = (t.k1 - t.k0 + SK - 1) / SK;
+        int KT = (t.k1 - t.k0 + SK - 1) / SK;
+        if constexpr (KG > 1) {
+            // a tile at a time: its sums go through the ring
+            KT = (KT + KG - 1) / KG;
+            LinTile mine = t;
+            mine.k0 = min(t.k1, t.k0 + SK * KT * set);
+            mine.k1 = min(t.k1, mine.k0 + SK * KT);
+            src = source_of(mine, true, it + 1);
+            slot = 0;
+            fill_ring();
+        }
         // Step: the slice in `slot`, its first fragments in fa0, fb0. The
         // first half computes on them, requests a slice into the slot before
         // (read to its end before the last barrier) and reads the second
@@ -445,13 +491,47 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
         else
             steps(std::false_type());
 
+        if constexpr (KG > 1) {
+            // the requests past the end (zeros) have landed; the other sets'
+            // sums, added in their order
+            wait_vmcnt<0>();
+            ring_barrier();
+            constexpr int NBLK = MB * NB;
+            const auto sums = [&](int from, int i, int q) {
+                return lds + ((((from - 1) * WAVES + wave) * NBLK + i) * 4 + q) * 1024 + 16 * lane;
+            };
+            if (set > 0 && !idle) {
+#pragma unroll
+                for (int i = 0; i < NBLK; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x16& v = acc[i / NB][i % NB];
+                        *reinterpret_cast<f32x4*>(sums(set, i, q)) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                    }
+            }
+            wait_vmcnt<0>();
+            ring_barrier();
+            if (set == 0 && !idle) {
+#pragma unroll
+                for (int f = 1; f < KG; ++f)
+#pragma unroll
+                    for (int i = 0; i < NBLK; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(sums(f, i, q));
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) acc[i / NB][i % NB][4 * q + u] += v[u];
+                        }
+            }
+        }
+        const bool store = !idle && set == 0;
         bool staged = false;
         if constexpr (kStage) staged = a.part_out == nullptr && !(PASS == kLinDw && a.out_f32);
         if (staged) {
             if constexpr (kStage) {
                 // the slot before is free until the next step's requests
-                if (!idle) {
-                    uint8_t* stage = lds + slot_after(slot, SLOTS - 1) * kSlot + wave * 4096;
+                if (store) {
+                    uint8_t* stage = lds + (KG > 1 ? kSums : slot_after(slot, SLOTS - 1) * kSlot) + wave * 4096;
                     if constexpr (PASS == kLinDh8)
                         store_tile_dh8<MB, NB>(a, t, mw, cw, stage, lane, acc);
                     else
@@ -460,9 +540,9 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                 relax = !idle && mw + S::WM <= t.rows && cw + S::WN <= a.N ? SLOTS - 2 : 0;
                 ring_barrier();  // every wave is done with its stage
                 // (read again, so that they take no registers in the epilogue)
-                first_fragments(slot * kSlot);
+                if constexpr (KG == 1) first_fragments(slot * kSlot);
             }
-        } else if (PASS <= kLinDw && !idle) {
+        } else if (PASS <= kLinDw && store) {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -472,6 +552,9 @@ __device__ __forceinline__ void linear_tiles(const LinearArgs& a, int bid, int n
                         store_block<T, PASS, kStage>(a, t.g, t.part, t.row0, t.rows, mw + 32 * mb + lr, cw + 32 * nb, lg,
                                              acc[mb][nb]);
                 }
+        }
+        if constexpr (KG > 1) {
+            if (!staged) ring_barrier();  // (the next tile's slices go where the sums were)
         }
     }
     // the requests past the last tile (zeros) land before the LDS is released
@@ -532,7 +615,7 @@ unsigned tile_grid(LinearArgs& a) {
 
 template <typename T, int PASS, class S>
 hipError_t launch(const LinearArgs& a0, hipStream_t st) {
-    constexpr int ring = S::SLOTS * lin_slot<S>();
+    constexpr int ring = lin_ring<S>();
     static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_tile_kernel<T, PASS, S>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (attr != hipSuccess) return attr;
@@ -545,7 +628,7 @@ hipError_t launch(const LinearArgs& a0, hipStream_t st) {
 
 template <typename T, class S>
 hipError_t launch_backward(const LinearArgs& x0, const LinearArgs& w0, const DbArgs& d, hipStream_t st) {
-    constexpr int ring = S::SLOTS * lin_slot<S>();
+    constexpr int ring = lin_ring<S>();
     static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_backward_kernel<T, S>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (attr != hipSuccess) return attr;
@@ -560,7 +643,7 @@ hipError_t launch_backward(const LinearArgs& x0, const LinearArgs& w0, const DbA
 
 template <int PASS, class S>
 hipError_t launch_pair(const LinearArgs& r0, const LinearArgs& s0, hipStream_t st) {
-    constexpr int ring = S::SLOTS * lin_slot<S>();
+    constexpr int ring = lin_ring<S>();
     static hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_pair_kernel<bf16_t, PASS, S>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (attr != hipSuccess) return attr;
@@ -593,7 +676,13 @@ hipError_t launch_pair_shape(const LinearArgs& r, const LinearArgs& s, int shape
 
 template <int PASS>
 hipError_t launch_pass(const LinearArgs& a, int shape, bool f32, hipStream_t st) {
-    if (f32) return shape == kLinTileMid ? launch<float, PASS, LinMid>(a, st) : launch<float, PASS, LinTiny>(a, st);
+    if (f32) {
+        switch (shape) {
+            case kLinTileMid: return launch<float, PASS, LinMid>(a, st);
+            case kLinTileTiny: return launch<float, PASS, LinTiny>(a, st);
+            default: return launch<float, PASS, LinSlim>(a, st);
+        }
+    }
     switch (shape) {
         case kLinTileBig: return launch<bf16_t, PASS, LinBig>(a, st);
         case kLinTileHalf: return launch<bf16_t, PASS, LinHalf>(a, st);
@@ -614,12 +703,12 @@ hipError_t launch_linear_pair(int pass, const LinearArgs& r, const LinearArgs& s
 }
 
 // dx, dW and db together (out or db NULL: not computed), 128 x 128 tiles in
-// bf16, 64 x 64 in float32, k not split
+// bf16, 64 x 32 in float32, k not split
 hipError_t launch_linear_backward(const LinearArgs& x, const LinearArgs& w, const DbArgs& d, bool f32, hipStream_t st) {
-    return f32 ? launch_backward<float, LinTiny>(x, w, d, st) : launch_backward<bf16_t, LinMid>(x, w, d, st);
+    return f32 ? launch_backward<float, LinSlim>(x, w, d, st) : launch_backward<bf16_t, LinMid>(x, w, d, st);
 }
 
-// shape: a LinTileShape (float32: Mid or Tiny; bf16: the others; dW: not Small)
+// shape: a LinTileShape (float32: Mid, Tiny or Slim; bf16: Big to Small; dW: not Small)
 hipError_t launch_linear_tile(int pass, const LinearArgs& a, int shape, bool f32, hipStream_t st) {
     switch (pass) {
         case kLinForward: return launch_pass<kLinForward>(a, shape, f32, st);
