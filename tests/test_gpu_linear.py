@@ -379,6 +379,34 @@ def test_the_residual_may_be_the_output():
     assert torch.equal(r.y, want)
 
 
+def test_one_workspace_for_layers_of_many_shapes():
+    """Calls of different shapes, k in parts or whole, take turns on one
+    buffer: the header is as before after every call, and so are the bits."""
+    mm = _mm()
+    shapes = [("f32", 80, 1336, 40, 1), ("bf16", 48, 4096, 1024, 64), ("bf16", 300, 4096, 520, 1), ("f32", 500, 4096, 260, 1),
+              ("bf16", 20000, 72, 136, 1), ("f32", 9000, 68, 132, 2), ("bf16", 600, 2048, 264, 7)]
+    layers = [Layer(rows, n_in, n_out, make_offsets(rows, G, "skewed" if G > 1 else "even", 3), kind, "gelu", seed=rows,
+                    device="cuda") for kind, rows, n_in, n_out, G in shapes]
+    runs = [Run(L, save="act") for L in layers]
+    ws = torch.randint(0, 256, (max(max(r.ws.numel(), r.bws.numel()) for r in runs),), dtype=torch.uint8, device="cuda")
+    mm.moe_workspace_init(ws)
+    want = None
+    for _ in range(4):
+        for r in runs:
+            r.ws = r.bws = ws
+            r.forward()
+            r.backward()
+            torch.cuda.synchronize()
+            assert not ws[:256].any()
+        got = [t.clone() for r in runs for t in (r.y, r.dx, r.dw, r.db)]
+        if want is None:
+            want = got
+            for r in runs:
+                r.check_forward()
+                r.check_backward()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_operands_past_4_gib():
     """Row offsets past 32 bits: 2.2 million rows of 1024 values, in two groups
     of very different size; checked on the first and the last rows, and the
