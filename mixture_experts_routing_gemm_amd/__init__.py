@@ -2,7 +2,10 @@
 
 gate (float32 logits, top-k, renormalised weights) -> dispatch (histogram,
 scan, stable permutation, optional per-token affine FP8 rows) -> grouped
-SwiGLU expert FFN (bf16 matrix cores) -> combine (weighted un-permute).
+SwiGLU expert FFN (bf16 matrix cores) -> combine (weighted un-permute), and
+the backward of these. Beside them: linear layers per expert or dense, forward
+and backward (moe_grouped_linear, moe_linear), and activation checkpoints in 8
+bits (moe_pack_rows8, moe_grouped_ffn_save8).
 The work runs in the HIP kernels of libmoe_mi355x.so behind the C ABI in
 include/moe.h; this package is its ctypes binding. Build the library with
 ``python mixture_experts_routing_gemm_amd/build.py``.

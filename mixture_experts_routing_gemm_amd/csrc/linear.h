@@ -434,11 +434,12 @@ __device__ __forceinline__ void part_range(int k_lo, int k_hi, int s, int parts,
 }
 
 // The position `i` of the list of work-group `bid` of `nblk` (a multiple of 8,
-// bid % 8 the XCD) -> tile, or false past its end. Forward and dx: the list of tiles (part by part, group by group) is cut into
-// eight equal runs, one for each XCD (work-groups b with b % 8 = x), dealt
-// round-robin to its work-groups: every m-tile takes equally long, and an
-// XCD's L2 sees few groups' weights. dW: tiles take as long as their group
-// has rows, so groups go longest first, and four tiles at a time to each XCD.
+// bid % 8 the XCD) -> tile, or false past its end. Forward and dx: the list of
+// tiles (part by part, group by group) is cut into eight equal runs, one for
+// each XCD (work-groups b with b % 8 = x), dealt round-robin to its
+// work-groups: every m-tile takes equally long, and an XCD's L2 sees few
+// groups' weights. dW: tiles take as long as their group has rows, so groups go
+// longest first, and four tiles at a time to each XCD.
 template <int PASS, int BM, int BN, int SK>
 __device__ __forceinline__ bool lin_tile(const LinearArgs& a, const GroupWalk& w, const GroupOrder& o, int bid, int nblk,
                                          int i, LinTile& t) {

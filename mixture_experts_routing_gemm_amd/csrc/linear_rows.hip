@@ -14,7 +14,9 @@
 // runs on the total.
 //
 // Rows past the group's end are not read (their lanes hold zeros): one row
-// costs 1/16 of the x traffic of 16.
+// costs 1/16 of the x traffic of 16. Measured: one row, 4096 -> 4096 in bf16,
+// 8.9 us, 3.8 TB/s with the launch; wider columns, k contiguous per wave and
+// non-temporal weight loads were no faster.
 #include <algorithm>
 
 #include "linear.h"
